@@ -500,6 +500,88 @@ RLT_API rlt_status rlt_paged_gather(const rlt_kv_pool *pool, int32_t bank, const
                             int32_t max_len, void *k_out, void *v_out, void *stream);
 
 /*
+ * ---------------------------------------------------------------- 8-bit cache
+ *
+ * A paged KV pool held in 8 bits, for models whose T banks per layer make the cache
+ * the largest thing on the device: e4m3 values with one power-of-two scale per row (a
+ * row is one token's head_dim keys, or values, of one kv head).  With a the row's
+ * largest magnitude (of the bf16 row handed in, for keys before their rotation),
+ *     e = max(floor(log2 a) - 7, -64)      (0 for a row of zeros),
+ *     held = e4m3(x * 2^-e), nearest even;  the exponent array holds e + 127;
+ * the row stands for held * 2^e.  A finite row never saturates.  A row with an
+ * infinity or NaN gets e = 121 (infinities held as 448, NaN as NaN).  Held rows
+ * are exact in bf16.  The pages' engines keep bf16; this format is the library's own.
+ * Pages, slots, page tables and banks as in rlt_kv_pool.
+ */
+typedef struct rlt_kv8_pool {
+    void *k;                /* e4m3 [num_banks][num_pages][num_kv_heads][page_size][head_dim] */
+    void *v;                /* same shape as k */
+    uint8_t *k_exp;         /* [num_banks][num_pages][num_kv_heads][page_size]: e + 127 of each key row */
+    uint8_t *v_exp;         /* of each value row */
+    int64_t num_pages;      /* num_pages*num_kv_heads*page_size at most 2^31 - 1 */
+    int32_t num_banks;
+    int32_t num_kv_heads;
+    int32_t page_size;      /* a multiple of 16 */
+    int32_t head_dim;       /* 64 or 128 */
+} rlt_kv8_pool;
+
+/*
+ * Append to an 8-bit pool with RoPE fused on queries and keys ([FFM] "LOTUS": store_kv
+ * to the handed slots; "Recurrent depth": one position for all of a token's banks).
+ * For i < n_tokens with out_loc[i] >= 0:
+ *   - query row i (num_q_heads heads) rotated, rounded to bf16 -> q_out[i]   (with q)
+ *   - key row i rotated, value row i as given, both quantised -> slot out_loc[i] of
+ *     the bank, and, where k_out / v_out is given, as bf16 exactly the values the pool
+ *     now stands for -> k_out[i], v_out[i]
+ * An entry with out_loc[i] < 0 writes nothing at all: its rows of q_out, k_out and
+ * v_out stay as they were.  So does one with out_loc[i] >= num_pages*page_size, which
+ * also sets RLT_DEVERR_BAD_SLOT.  Slots within one call must be distinct.
+ *   q, k_new, v_new  bf16 token rows of num_q_heads / num_kv_heads x head_dim elements,
+ *                    *_stride elements from token to token (multiples of 8), so that
+ *                    the three may be views of one fused projection; q may be NULL
+ *                    (then q_out is too)
+ *   q_out            bf16 [n_tokens][num_q_heads][head_dim]
+ *   k_out, v_out     NULL, or bf16 [n_tokens][num_kv_heads][head_dim]
+ *   positions        int64 [n_tokens], any value; may be NULL with rot_dim == 0
+ *   rot_dim          even, 0 (no rotation) .. head_dim; pairs (i, i + rot_dim/2) turn by
+ *                    positions[i] * rope_base^(-2i/rot_dim), as rlt_kv_append_rope.
+ *                    The angle is reduced modulo a turn in 64-bit fixed point; sin, cos
+ *                    and the rotation are fp32: off by about 2^-23 of the pair's norm
+ *                    before the one rounding to bf16 or e4m3
+ *   request, written, batch  as rlt_kv_append_rope
+ * An output may be the call's own input of the same kind (same address, rows
+ * num_heads*head_dim apart); any other overlap is RLT_ERR_INVALID_ARG.  All arrays but
+ * positions, out_loc, request and written (their elements' alignment) 16-byte aligned.
+ */
+RLT_API rlt_status rlt_kv8_append_rope(const rlt_kv8_pool *pool, int32_t bank, const void *q, int32_t num_q_heads,
+                                       int64_t q_stride, const void *k_new, int64_t k_stride, const void *v_new,
+                                       int64_t v_stride, const int64_t *positions, const int64_t *out_loc,
+                                       int32_t n_tokens, int32_t rot_dim, double rope_base, void *q_out, void *k_out,
+                                       void *v_out, const int32_t *request, int32_t *written, int32_t batch,
+                                       void *stream);
+
+/* Bytes of device workspace rlt_paged_decode_attn_kv8 needs; 0 for invalid sizes. */
+RLT_API size_t rlt_paged_decode_kv8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t max_seq_len, int32_t split_tokens);
+
+/*
+ * Paged GQA decode attention over an 8-bit pool: rlt_paged_decode_attn's computation with
+ * K_j and V_j the values the pool stands for.  Arguments, workspace, flags, the clamping
+ * of lengths and the skipping of bad pages as there, without the fused append (the
+ * new token's rows are appended first, by rlt_kv8_append_rope; so RLT_ATTN_EARLY_START
+ * only where that append is not among the kernels that may still run).  Supported:
+ * head_dim 64 or 128; any num_q_heads/num_kv_heads from 1 to 8.  Scores and sums
+ * are fp32; a query enters with its bf16 bits down to 2^-38 of its head's largest
+ * magnitude, a weight with 11 bits down to 2^-28 of the largest weight x value scale.
+ * Rows of the pool behind a request's end are not looked at, whatever they hold.
+ */
+RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t bank, const void *q,
+                                             int32_t num_q_heads, const int32_t *page_table, int32_t max_pages,
+                                             const int32_t *seq_lens, int32_t batch, int32_t max_seq_len, float scale,
+                                             void *out, float *lse_out, void *workspace, size_t workspace_bytes,
+                                             int32_t split_tokens, uint32_t flags, void *stream);
+
+/*
  * HOST validation of a decode batch before it is handed to the GPU (all
  * arrays are host copies): every page-table entry a request uses lies in
  * [0, num_pages); seq_lens[b] in [0, max_pages*page_size]; every

@@ -14,6 +14,8 @@ Functions keep the C names:
 * ``rlt_latent_noise_init`` position-keyed truncated-normal latent noise.
 * ``rlt_noise_hash24``      the 24-bit uniforms behind that noise.
 * ``rlt_paged_gather``      page-table gather into dense rows (for checks).
+* ``rlt_kv8_append_rope``   RoPE on queries and keys + append to an 8-bit pool (``KV8Pool``).
+* ``rlt_paged_decode_attn_kv8``  paged decode attention over an 8-bit pool.
 * ``rlt_validate_batch``    host validation of page tables and append slots.
 * ``rlt_get_device_error``  read and clear the kernels' error bits.
 """
@@ -31,6 +33,7 @@ __all__ = [
     "rlt_noise_hash24", "rlt_paged_gather", "rlt_validate_batch", "rlt_get_device_error", "rlt_debug_fault_next_decode",
     "rlt_version", "PrefixPlan", "rlt_plan_prefix", "rlt_choose_chunk_tiles", "rlt_paged_decode_attn_prefix",
     "rlt_paged_decode_prefix_workspace_size", "rlt_kv_append_rope", "rlt_publishable_prefix",
+    "KV8Pool", "rlt_kv8_append_rope", "rlt_paged_decode_kv8_workspace_size", "rlt_paged_decode_attn_kv8",
     "ExtendPlan", "rlt_plan_extend", "rlt_paged_extend_attn", "ATTN_EARLY_START", "DEVERR_BAD_PAGE", "DEVERR_BAD_SLOT", "DEVERR_TIMEOUT", "DEVERR_BAD_LEN",
 ]
 
@@ -55,6 +58,12 @@ class rlt_kv_pool(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class rlt_kv8_pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("num_banks", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 RLT_BF16 = 0
 
 
@@ -77,6 +86,7 @@ def load():
     P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     u32 = ctypes.c_uint32
     pool_p = ctypes.POINTER(rlt_kv_pool)
+    pool8_p = ctypes.POINTER(rlt_kv8_pool)
     sigs = {
         "rlt_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "rlt_version": (i32, []),
@@ -101,6 +111,11 @@ def load():
         "rlt_debug_fault_next_decode": (ctypes.c_int, [ctypes.c_uint64]),
         "rlt_kv_append_rope": (ctypes.c_int, [pool_p, i32, P, P, P, P, i32, i32, ctypes.c_double, P, P, i32, P]),
         "rlt_publishable_prefix": (ctypes.c_int, [P, i32, i32, i32, P, P]),
+        "rlt_kv8_append_rope": (ctypes.c_int, [pool8_p, i32, P, i32, i64, P, i64, P, i64, P, P, i32, i32,
+                                               ctypes.c_double, P, P, P, P, P, i32, P]),
+        "rlt_paged_decode_kv8_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
+        "rlt_paged_decode_attn_kv8": (ctypes.c_int, [pool8_p, i32, P, i32, P, i32, P, i32, i32, f32, P, P, P, sz, i32,
+                                                     u32, P]),
         "rlt_plan_extend": (ctypes.c_int, [P, P, i32, i32, i32, i32, P, i32, P, P, i32, P, P, P]),
         "rlt_paged_extend_workspace_size": (sz, [i32, i32, i32, i32]),
         "rlt_paged_extend_attn": (ctypes.c_int, [pool_p, i32, P, i32, i32, P, i32, i32, P, P, P, P, P, i32, i32,
@@ -582,4 +597,154 @@ def rlt_paged_extend_attn(pool: KVPool, bank: int, q, page_table, plan: ExtendPl
         max(plan.max_slots, 1), plan.chunk_tiles, float(scale), _dev(out, torch.bfloat16, "out"), lse_ptr,
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(), int(max_ctas),
         ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_paged_extend_attn")
+    return out
+
+
+# ------------------------------------------------------------- 8-bit cache
+
+class KV8Pool:
+    """A paged KV pool held in 8 bits: float8_e4m3fn CUDA tensors k, v [banks][pages][Hkv][page_size][D]
+    and uint8 k_exp, v_exp [banks][pages][Hkv][page_size]; a row stands for its e4m3 values times
+    2^(exp - 127) (include/rlt.h, "8-bit cache")."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        import torch
+        if k.shape != v.shape or k.dim() != 5 or k_exp.shape != k.shape[:4] or v_exp.shape != k.shape[:4]:
+            raise ValueError("k and v must both be [banks][pages][kv_heads][page_size][head_dim], "
+                             "k_exp and v_exp [banks][pages][kv_heads][page_size]")
+        for name, t, dt in (("k", k, torch.float8_e4m3fn), ("v", v, torch.float8_e4m3fn),
+                            ("k_exp", k_exp, torch.uint8), ("v_exp", v_exp, torch.uint8)):
+            _dev(t, dt, name)
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.device = _same_device(k, v, k_exp, v_exp)
+        nb, P, Hkv, ps, D = k.shape
+        self.num_banks, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = nb, P, Hkv, ps, D
+        self.struct = rlt_kv8_pool(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), P, nb, Hkv, ps, D)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, num_banks, num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
+        """A pool of uninitialised rows (a row is defined once it has been appended)."""
+        import torch
+        shape = (num_banks, num_pages, num_kv_heads, page_size, head_dim)
+        return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
+                   *(torch.empty(shape[:4], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def _same_device(*tensors):
+    """The device of these tensors (None entries aside); they must share it, and it must be the current one:
+    the library launches on the current device."""
+    import torch
+    found = None
+    for t in tensors:
+        if t is None:
+            continue
+        if found is None:
+            found = t.device
+        elif t.device != found:
+            raise ValueError(f"tensors on {found} and {t.device} in one call")
+    if found is not None and found.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {found}, but the current device is cuda:{torch.cuda.current_device()}")
+    return found
+
+
+def _record(stream, *made):
+    """Tensors this call made on torch's current stream and uses on `stream`: tell the allocator."""
+    import torch
+    if stream is None:
+        return
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in made:
+        if t is not None:
+            s.wait_stream(torch.cuda.current_stream())
+            t.record_stream(s)
+
+
+def _token_rows(t, heads, D, n, name):
+    """(pointer, token stride) of bf16 [n][heads][D] rows whose heads are contiguous (a view of a fused projection)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    if tuple(t.shape) != (n, heads, D):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] = {(n, heads, D)}, got {tuple(t.shape)}")
+    if n > 0 and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * D)
+
+
+def _ptr(t, dtype, name, shape=None):
+    """Device address of a contiguous tensor of this type and shape, or 0 for None."""
+    if t is None:
+        return 0
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return _dev(t, dtype, name).value or 0
+
+
+def rlt_kv8_append_rope(pool: KV8Pool, bank: int, k_new, v_new, positions, out_loc, rot_dim: int, rope_base: float,
+                        q=None, q_out=None, k_out=None, v_out=None, request=None, written=None, stream=None):
+    """Append to an 8-bit pool with RoPE on keys and queries: k_new/v_new bf16 [N][Hkv][D], q bf16 [N][Hq][D]
+    (views of one projection allowed), positions and out_loc int64 [N] (negative slot = nothing is written for
+    the entry).  q_out: the rotated queries (made if q is given without it: zeros where an entry is skipped);
+    k_out / v_out (optional): bf16 [N][Hkv][D], the rows as the pool holds them.  Returns q_out (None without q)."""
+    import torch
+    n, Hkv, D = int(out_loc.numel()), pool.num_kv_heads, pool.head_dim
+    kp, ks = _token_rows(k_new, Hkv, D, n, "k_new")
+    vp, vs = _token_rows(v_new, Hkv, D, n, "v_new")
+    Hq, qp, qs = 0, 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens][heads][head_dim]")
+        Hq = int(q.shape[1])
+        qp, qs = _token_rows(q, Hq, D, n, "q")
+        if q_out is None:
+            q_out = torch.zeros((n, Hq, D), dtype=torch.bfloat16, device=q.device)
+            _record(stream, q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(pool.k, k_new, v_new, positions, out_loc, q, q_out, k_out, v_out, request, written)
+    batch = 0
+    if written is not None:
+        if written.dim() != 2 or written.shape[0] != pool.num_banks or request is None:
+            raise ValueError("written must be [num_banks][batch] and needs request")
+        batch = int(written.shape[1])
+    _check(load().rlt_kv8_append_rope(
+        pool.ref, bank, qp, Hq, qs, kp, ks, vp, vs, _ptr(positions, torch.int64, "positions", (n,)),
+        _ptr(out_loc, torch.int64, "out_loc", (n,)), n, int(rot_dim), float(rope_base),
+        _ptr(q_out, torch.bfloat16, "q_out", (n, Hq, D)), _ptr(k_out, torch.bfloat16, "k_out", (n, Hkv, D)),
+        _ptr(v_out, torch.bfloat16, "v_out", (n, Hkv, D)), _ptr(request, torch.int32, "request", (n,)),
+        _ptr(written, torch.int32, "written"), batch, _stream(stream)), "rlt_kv8_append_rope")
+    return q_out
+
+
+def rlt_paged_decode_kv8_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                        split_tokens=0) -> int:
+    return int(load().rlt_paged_decode_kv8_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                                          split_tokens))
+
+
+def rlt_paged_decode_attn_kv8(pool: KV8Pool, bank: int, q, page_table, seq_lens, max_seq_len: int, out=None,
+                              lse_out=None, workspace=None, scale: float = 0.0, split_tokens: int = 0, stream=None,
+                              early_start: bool = False):
+    """Paged decode attention over one bank of an 8-bit pool; arguments as rlt_paged_decode_attn."""
+    import torch
+    _check_q_out(pool, q, out, lse_out)
+    B, Hq, D = q.shape
+    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("page_table must be [B][max_pages] and seq_lens [B]")
+    if out is None:
+        out = torch.empty_like(q)
+        _record(stream, out)
+    if workspace is None:
+        need = rlt_paged_decode_kv8_workspace_size(B, Hq, pool.num_kv_heads, D, max_seq_len, split_tokens)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
+        _record(stream, workspace)
+    _same_device(pool.k, q, page_table, seq_lens, out, lse_out, workspace)
+    _check(load().rlt_paged_decode_attn_kv8(
+        pool.ref, bank, _ptr(q, torch.bfloat16, "q"), Hq, _ptr(page_table, torch.int32, "page_table"),
+        page_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), B, int(max_seq_len), float(scale),
+        _ptr(out, torch.bfloat16, "out"), _ptr(lse_out, torch.float32, "lse_out"),
+        workspace.data_ptr() if workspace is not None else 0,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, int(split_tokens),
+        ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_paged_decode_attn_kv8")
     return out

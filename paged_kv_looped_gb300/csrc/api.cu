@@ -178,9 +178,45 @@ rlt_status validate_attention_batch(const int32_t *page_table, int32_t max_pages
                               page_size);
 }
 
+// Append slots: inside the pool (negative: no token) and distinct.
+rlt_status check_slots(const int64_t *out_loc, int32_t n_tokens, int64_t num_slots, cudaStream_t stream)
+{
+    rlt_status st = RLT_OK;
+    if (!fetch_for_validation(stream, &st))
+        return st;
+    std::vector<int64_t> loc;
+    if (!copy_to_host(loc, out_loc, (size_t)n_tokens))
+        return RLT_ERR_CUDA;
+    std::unordered_set<int64_t> seen;
+    for (const int64_t slot : loc) {
+        if (slot < 0)
+            continue;
+        if (slot >= num_slots)
+            return RLT_ERR_OUT_OF_RANGE;
+        if (!seen.insert(slot).second)
+            return RLT_ERR_INVALID_ARG;          // two tokens written to one slot
+    }
+    return RLT_OK;
+}
+
 }  // namespace
 
 namespace rlt {
+
+rlt_status current_device_info(unsigned int **err, int *num_sms) { return device_info(err, num_sms); }
+
+rlt_status validate_slots(const int64_t *out_loc, int32_t n_tokens, int64_t num_slots, cudaStream_t stream)
+{
+    return validate_enabled() ? check_slots(out_loc, n_tokens, num_slots, stream) : RLT_OK;
+}
+
+rlt_status validate_lengths(const int32_t *page_table, int32_t max_pages, const int32_t *seq_lens, int32_t batch,
+                            int64_t num_pages, int32_t page_size, cudaStream_t stream)
+{
+    return validate_enabled() ? validate_attention_batch(page_table, max_pages, seq_lens, batch, num_pages, page_size,
+                                                         false, stream)
+                              : RLT_OK;
+}
 
 rlt_status check_decode_args(const rlt_kv_pool *pool, int32_t bank, const void *q, const void *k_new,
                              const void *v_new, int32_t num_q_heads, const int32_t *page_table, int32_t max_pages,
@@ -270,24 +306,9 @@ RLT_API rlt_status rlt_kv_append(const rlt_kv_pool *pool, int32_t bank, const vo
         return RLT_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || reinterpret_cast<uintptr_t>(out_loc) % 8 != 0)
         return RLT_ERR_INVALID_ARG;
-    if (validate_enabled()) {
-        std::vector<int64_t> loc;
-        if (fetch_for_validation(static_cast<cudaStream_t>(stream), &st)) {
-            if (!copy_to_host(loc, out_loc, (size_t)n_tokens))
-                return RLT_ERR_CUDA;
-            std::unordered_set<int64_t> seen;
-            for (const int64_t slot : loc) {
-                if (slot < 0)
-                    continue;
-                if (slot >= pool->num_pages * pool->page_size)
-                    return RLT_ERR_OUT_OF_RANGE;
-                if (!seen.insert(slot).second)
-                    return RLT_ERR_INVALID_ARG;   // two tokens written to one slot
-            }
-        } else if (st != RLT_OK) {
-            return st;
-        }
-    }
+    if ((st = rlt::validate_slots(out_loc, n_tokens, pool->num_pages * pool->page_size,
+                                  static_cast<cudaStream_t>(stream))) != RLT_OK)
+        return st;
     unsigned int *err = nullptr;
     if ((st = device_info(&err, nullptr)) != RLT_OK)
         return st;

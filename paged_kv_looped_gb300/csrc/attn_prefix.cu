@@ -858,30 +858,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
 // ---------------------------------------------------------- tensor maps
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
-    });
-    return fn;
-}
-
 // 2-D view of one bank: rows of head_dim = 128 bf16, boxes of 64 x box_rows, 128B swizzle.
 bool make_map(CUtensorMap *map, const void *bank, int64_t rows, int box_rows)
 {
-    EncodeTiledFn fn = encode_fn();
+    const tc::EncodeTiledFn fn = tc::encode_tiled_fn();
     if (fn == nullptr)
         return false;
     const cuuint64_t dims[2] = {128, (cuuint64_t)rows};

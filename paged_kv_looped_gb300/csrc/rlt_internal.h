@@ -174,4 +174,58 @@ cudaError_t launch_noise(float *out, uint32_t *hash_out, const uint64_t *seeds,
                          const int64_t *positions, int64_t n_rows, int32_t channels,
                          float initializer_range, cudaStream_t stream);
 
+// Error word and SM count of the current device (looked up once per device).
+rlt_status current_device_info(unsigned int **err, int *num_sms);
+
+// RLT_VALIDATE=1: host checks of device arrays before a launch (see rlt.h).  validate_slots:
+// append slots inside the pool and distinct; validate_lengths: page-table entries and lengths.
+// RLT_OK where the mode is off or the stream is being captured.
+rlt_status validate_slots(const int64_t *out_loc, int32_t n_tokens, int64_t num_slots, cudaStream_t stream);
+rlt_status validate_lengths(const int32_t *page_table, int32_t max_pages, const int32_t *seq_lens, int32_t batch,
+                            int64_t num_pages, int32_t page_size, cudaStream_t stream);
+
+// ------------------------------------------------------------ 8-bit cache
+
+struct Kv8AppendParams {
+    const uint16_t *q;           // token rows of num_q_heads x D, q_stride elements apart; null: no queries
+    const uint16_t *k_new;       // token rows of num_kv_heads x D
+    const uint16_t *v_new;
+    int64_t q_stride, k_stride, v_stride;
+    const int64_t *positions;    // [n_tokens]
+    const int64_t *out_loc;      // [n_tokens]
+    uint8_t *k_bank;             // bank base: e4m3 [num_pages][Hkv][ps][D]
+    uint8_t *v_bank;
+    uint8_t *k_exp;              // bank base: [num_pages][Hkv][ps]
+    uint8_t *v_exp;
+    uint16_t *q_out;             // [n_tokens][num_q_heads][D]
+    uint16_t *k_out;             // [n_tokens][num_kv_heads][D] or null: the rows as held
+    uint16_t *v_out;
+    const int32_t *request;
+    int32_t *written;            // this bank's counters or null
+    unsigned int *err;
+    int64_t num_slots;
+    int32_t n_tokens;
+    int32_t num_q_heads;         // 0 without q
+    int32_t num_kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t batch;
+    uint64_t freq[64];           // rope_frequencies
+};
+
+// One bank of an 8-bit pool.
+struct Kv8Bank {
+    const uint8_t *k, *v;        // e4m3 [num_pages][Hkv][ps][D]
+    const uint8_t *k_exp, *v_exp;
+};
+
+// Decode over an 8-bit bank: p as for launch_decode (k_bank, v_bank unused), plan_decode's sizes.
+bool kv8_decode_supported(int head_dim, int group);
+cudaError_t launch_kv8_decode(const DecodeParams &p, const Kv8Bank &bank, int head_dim, cudaStream_t stream,
+                              bool early);
+
+void rope_frequencies(int rot_dim, double base, uint64_t *freq);
+cudaError_t launch_kv8_append(const Kv8AppendParams &p, cudaStream_t stream);
+
 }  // namespace rlt

@@ -18,6 +18,13 @@
 namespace rlt {
 namespace tc {
 
+// ---------------------------------------------------------------- tensor maps (host)
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();                 // null if the driver has none
+
 // ---------------------------------------------------------------- TMA tiles
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map)
 {
