@@ -582,6 +582,41 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
                                              int32_t split_tokens, uint32_t flags, void *stream);
 
 /*
+ * Causal attention over packed prompts, straight from the projection's rows ([FFM] "LOTUS":
+ * a prompt is one parallel pass over all its positions).  Row i of a sequence attends to
+ * the sequence's rows 0..i: out = softmax(scale <q, K>) V, GQA as in rlt_paged_decode_attn.
+ * It reads no pool: the prompt attention of an 8-bit cache (with rlt_kv8_append_rope's
+ * q_out, k_out, v_out it sees the values later decode calls will see), and of head_dim 64.
+ *
+ * rlt_plan_prefill (HOST arrays): the work items of a batch of sequences that lie one after
+ * another, for query_group = num_q_heads / num_kv_heads: items int32 [sizes[0]][4] = first
+ * row of the sequence, its length, first query row of the item, 0; sizes[0..1] = items, rows.
+ * Returns RLT_ERR_OUT_OF_RANGE when max_items is too small (sizes filled),
+ * RLT_ERR_INVALID_ARG for a negative length, RLT_ERR_UNSUPPORTED past 2^31 - 1 rows.
+ *
+ *   q, k, v    bf16 token rows of num_q_heads / num_kv_heads x head_dim elements, *_stride
+ *              elements from token to token (multiples of 8): views of one fused
+ *              projection may be handed in.  16-byte aligned
+ *   num_rows   rows of q, k, v, out; at least the plan's.  Rows behind the last sequence
+ *              are neither looked at nor written
+ *   items      the plan, DEVICE copy; an item outside num_rows is skipped and sets
+ *              RLT_DEVERR_BAD_LEN
+ *   scale      softmax scale; <= 0 means 1/sqrt(head_dim)
+ *   out        bf16 [num_rows][num_q_heads][head_dim], 16-byte aligned, apart from q, k, v
+ *   lse_out    fp32 [num_rows][num_q_heads], natural log, or NULL
+ *   flags      0 or RLT_ATTN_EARLY_START (no kernel still running ahead may write items)
+ * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
+ * fp32, weights enter the product with V as bf16.
+ */
+RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t batch, int32_t query_group, int32_t *items,
+                                    int32_t max_items, int32_t *sizes);
+
+RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t q_stride, const void *k,
+                                    int64_t k_stride, const void *v, int64_t v_stride, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t num_rows, const int32_t *items, int32_t num_items,
+                                    float scale, void *out, float *lse_out, uint32_t flags, void *stream);
+
+/*
  * HOST validation of a decode batch before it is handed to the GPU (all
  * arrays are host copies): every page-table entry a request uses lies in
  * [0, num_pages); seq_lens[b] in [0, max_pages*page_size]; every

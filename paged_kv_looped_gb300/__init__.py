@@ -16,6 +16,7 @@ Functions keep the C names:
 * ``rlt_paged_gather``      page-table gather into dense rows (for checks).
 * ``rlt_kv8_append_rope``   RoPE on queries and keys + append to an 8-bit pool (``KV8Pool``).
 * ``rlt_paged_decode_attn_kv8``  paged decode attention over an 8-bit pool.
+* ``rlt_prefill_attn``      causal attention over packed prompts (plan: ``rlt_plan_prefill``).
 * ``rlt_validate_batch``    host validation of page tables and append slots.
 * ``rlt_get_device_error``  read and clear the kernels' error bits.
 """
@@ -34,6 +35,7 @@ __all__ = [
     "rlt_version", "PrefixPlan", "rlt_plan_prefix", "rlt_choose_chunk_tiles", "rlt_paged_decode_attn_prefix",
     "rlt_paged_decode_prefix_workspace_size", "rlt_kv_append_rope", "rlt_publishable_prefix",
     "KV8Pool", "rlt_kv8_append_rope", "rlt_paged_decode_kv8_workspace_size", "rlt_paged_decode_attn_kv8",
+    "PrefillPlan", "rlt_plan_prefill", "rlt_prefill_attn",
     "ExtendPlan", "rlt_plan_extend", "rlt_paged_extend_attn", "ATTN_EARLY_START", "DEVERR_BAD_PAGE", "DEVERR_BAD_SLOT", "DEVERR_TIMEOUT", "DEVERR_BAD_LEN",
 ]
 
@@ -116,6 +118,8 @@ def load():
         "rlt_paged_decode_kv8_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
         "rlt_paged_decode_attn_kv8": (ctypes.c_int, [pool8_p, i32, P, i32, P, i32, P, i32, i32, f32, P, P, P, sz, i32,
                                                      u32, P]),
+        "rlt_plan_prefill": (ctypes.c_int, [P, i32, i32, P, i32, P]),
+        "rlt_prefill_attn": (ctypes.c_int, [P, i32, i64, P, i64, P, i64, i32, i32, i32, P, i32, f32, P, P, u32, P]),
         "rlt_plan_extend": (ctypes.c_int, [P, P, i32, i32, i32, i32, P, i32, P, P, i32, P, P, P]),
         "rlt_paged_extend_workspace_size": (sz, [i32, i32, i32, i32]),
         "rlt_paged_extend_attn": (ctypes.c_int, [pool_p, i32, P, i32, i32, P, i32, i32, P, P, P, P, P, i32, i32,
@@ -747,4 +751,67 @@ def rlt_paged_decode_attn_kv8(pool: KV8Pool, bank: int, q, page_table, seq_lens,
         workspace.data_ptr() if workspace is not None else 0,
         workspace.numel() * workspace.element_size() if workspace is not None else 0, int(split_tokens),
         ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_paged_decode_attn_kv8")
+    return out
+
+
+# ---------------------------------------------------------- packed prompts
+
+class PrefillPlan:
+    """Host output of rlt_plan_prefill; .to(device) uploads it for rlt_prefill_attn."""
+
+    def __init__(self, items, num_rows, query_group):
+        self.items, self.num_items, self.num_rows, self.query_group = items, len(items), num_rows, query_group
+        self.dev = None
+
+    def to(self, device):
+        import torch
+        self.dev = torch.from_numpy(self.items).to(device)
+        return self
+
+
+def rlt_plan_prefill(seq_lens, query_group: int = 1) -> PrefillPlan:
+    """Work items of causal attention over sequences of these lengths, packed one after another.
+    ``query_group`` = num_q_heads / num_kv_heads of the attention the plan is for."""
+    sl, slp = _host(seq_lens, np.int32)
+    sizes = np.zeros(2, np.int32)
+    st = load().rlt_plan_prefill(slp, sl.size, int(query_group), ctypes.c_void_p(0), 0, _np_ptr(sizes))
+    if st not in (0, 2):
+        _check(st, "rlt_plan_prefill")
+    items = np.zeros((int(sizes[0]), 4), np.int32)
+    _check(load().rlt_plan_prefill(slp, sl.size, int(query_group), _np_ptr(items), items.shape[0], _np_ptr(sizes)),
+           "rlt_plan_prefill")
+    return PrefillPlan(items, int(sizes[1]), int(query_group))
+
+
+def _np_ptr(a):
+    return a.ctypes.data_as(ctypes.c_void_p)
+
+
+def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: float = 0.0, stream=None,
+                     early_start: bool = False):
+    """Causal attention over packed prompts: q bf16 [N][Hq][D], k/v bf16 [N][Hkv][D] (views of one projection
+    allowed), N >= the plan's rows; rows behind the last sequence are left alone (zeros in an out made here).
+    Returns out [N][Hq][D]."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens][heads][head_dim]")
+    N, Hq, D = q.shape
+    Hkv = int(k.shape[1])
+    qp, qs = _token_rows(q, Hq, D, N, "q")
+    kp, ks = _token_rows(k, Hkv, D, N, "k")
+    vp, vs = _token_rows(v, Hkv, D, N, "v")
+    if N < plan.num_rows:
+        raise ValueError("the plan was built for more rows")
+    if plan.num_items and plan.query_group * Hkv != Hq:
+        raise ValueError("the plan was built for another query group")
+    if plan.dev is None:
+        plan.to(q.device)
+    if out is None:
+        out = (torch.empty if N == plan.num_rows else torch.zeros)((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+        _record(stream, out)
+    _same_device(q, k, v, plan.dev, out, lse_out)
+    _check(load().rlt_prefill_attn(
+        qp, Hq, qs, kp, ks, vp, vs, Hkv, D, N, _ptr(plan.dev, torch.int32, "plan"), plan.num_items, float(scale),
+        _ptr(out, torch.bfloat16, "out", (N, Hq, D)), _ptr(lse_out, torch.float32, "lse_out", (N, Hq)),
+        ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_prefill_attn")
     return out

@@ -1,4 +1,4 @@
-// extern "C" entry points of the 8-bit cache: host-side argument checks and dispatch to the
+// extern "C" entry points of the 8-bit cache and of packed prompts: host-side argument checks and dispatch to the
 // kernels.  Nothing here allocates device memory.
 #include <cuda_runtime.h>
 
@@ -194,6 +194,53 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
     p.qscale = (float)(s * 1.4426950408889634);   // log2(e): softmax in base 2
     return from_cuda(rlt::launch_kv8_decode(p, b8, pool->head_dim, static_cast<cudaStream_t>(stream),
                                             (flags & RLT_ATTN_EARLY_START) != 0));
+}
+
+RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t q_stride, const void *k,
+                                    int64_t k_stride, const void *v, int64_t v_stride, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t num_rows, const int32_t *items, int32_t num_items,
+                                    float scale, void *out, float *lse_out, uint32_t flags, void *stream)
+{
+    if ((flags & ~RLT_ATTN_EARLY_START) != 0 || num_rows < 0 || num_items < 0 || num_kv_heads < 1 || num_q_heads < 1 ||
+        num_q_heads % num_kv_heads != 0 || !std::isfinite(scale))
+        return RLT_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || (int64_t)num_items * num_q_heads > INT32_MAX)
+        return RLT_ERR_UNSUPPORTED;
+    if (num_items == 0)
+        return RLT_OK;
+    const int64_t q_width = (int64_t)num_q_heads * head_dim, kv_width = (int64_t)num_kv_heads * head_dim;
+    if (num_rows < 1 || q == nullptr || k == nullptr || v == nullptr || items == nullptr || out == nullptr ||
+        !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+        reinterpret_cast<uintptr_t>(items) % 4 != 0 || reinterpret_cast<uintptr_t>(lse_out) % 4 != 0)
+        return RLT_ERR_INVALID_ARG;
+    if (q_stride < q_width || k_stride < kv_width || v_stride < kv_width || q_stride % 8 != 0 || k_stride % 8 != 0 ||
+        v_stride % 8 != 0)
+        return RLT_ERR_INVALID_ARG;
+    const Block to{out, num_rows, q_width, q_width};
+    if (clashes(to, {q, num_rows, q_width, q_stride}, false) || clashes(to, {k, num_rows, kv_width, k_stride}, false) ||
+        clashes(to, {v, num_rows, kv_width, v_stride}, false))
+        return RLT_ERR_INVALID_ARG;
+    rlt::PrefillParams p{};
+    rlt_status st = rlt::current_device_info(&p.err, nullptr);
+    if (st != RLT_OK)
+        return st;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.items = items;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse_out = lse_out;
+    p.num_rows = num_rows;
+    p.num_items = num_items;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_dim);
+    p.qscale = (float)(s * 1.4426950408889634);   // log2(e): softmax in base 2
+    return from_cuda(rlt::launch_prefill(p, head_dim, static_cast<cudaStream_t>(stream),
+                                         (flags & RLT_ATTN_EARLY_START) != 0));
 }
 
 }  // extern "C"

@@ -225,6 +225,21 @@ bool kv8_decode_supported(int head_dim, int group);
 cudaError_t launch_kv8_decode(const DecodeParams &p, const Kv8Bank &bank, int head_dim, cudaStream_t stream,
                               bool early);
 
+// ------------------------------------------------------- packed prompts
+
+struct PrefillParams {
+    const uint16_t *q, *k, *v;   // token rows, *_stride elements apart
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *items;        // rlt_plan_prefill
+    uint16_t *out;               // [num_rows][num_q_heads][D]
+    float *lse_out;              // [num_rows][num_q_heads] or null
+    unsigned int *err;
+    int32_t num_rows, num_items, num_q_heads, num_kv_heads;
+    float qscale;                // softmax scale * log2(e)
+};
+
+cudaError_t launch_prefill(const PrefillParams &p, int head_dim, cudaStream_t stream, bool early);
+
 void rope_frequencies(int rot_dim, double base, uint64_t *freq);
 cudaError_t launch_kv8_append(const Kv8AppendParams &p, cudaStream_t stream);
 

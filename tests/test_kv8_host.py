@@ -88,6 +88,52 @@ def test_decode_of_nothing(lib):
     assert decode(lib, b=0, q=0, out=0) == OK
 
 
+def prefill(lib, **kw):
+    f = dict(q=A, hq=4, qs=512, k=A * 2, ks=256, v=A * 3, vs=256, hkv=2, d=128, n=300, items=A * 4, ni=3, scale=0.0,
+             out=A * 5, lse=A * 6, flags=0)
+    f.update(kw)
+    return lib.rlt_prefill_attn(f["q"], f["hq"], f["qs"], f["k"], f["ks"], f["v"], f["vs"], f["hkv"], f["d"], f["n"],
+                                f["items"], f["ni"], f["scale"], f["out"], f["lse"], f["flags"], 0)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(flags=4), INVALID), (dict(n=-1), INVALID), (dict(ni=-1), INVALID), (dict(hkv=0), INVALID), (dict(hq=5), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(d=96), UNSUPPORTED), (dict(ni=1 << 30), UNSUPPORTED), (dict(n=0), INVALID),
+    (dict(q=0), INVALID), (dict(v=0), INVALID), (dict(items=0), INVALID), (dict(out=0), INVALID), (dict(k=A + 2), INVALID),
+    (dict(items=A + 2), INVALID), (dict(lse=A + 1), INVALID), (dict(qs=256), INVALID), (dict(ks=260), INVALID),
+    (dict(out=A), INVALID), (dict(out=A * 2 - 1024), INVALID)])
+def test_prefill_refusals(lib, change, status):
+    assert prefill(lib, **change) == status
+
+
+def test_prefill_of_nothing(lib):
+    assert prefill(lib, ni=0, n=0, q=0, out=0) == OK
+
+
+@pytest.mark.parametrize("group,step", [(1, 256), (2, 128), (3, 256), (8, 128)])
+def test_prefill_plan(lib, group, step):
+    lens = [300, 0, 1, 1000, 128, 256]
+    plan = rlt.rlt_plan_prefill(lens, group)
+    first = np.concatenate([[0], np.cumsum(lens)[:-1]])
+    want = {(int(first[b]), n, q0, 0) for b, n in enumerate(lens) for q0 in range(0, n, step)}
+    assert plan.num_rows == sum(lens) and len(plan.items) == len(want)
+    assert {tuple(int(x) for x in it) for it in plan.items} == want
+    assert (np.diff(plan.items[:, 2]) <= 0).all()               # the items with the most keys first
+    assert rlt.rlt_plan_prefill([], group).num_items == 0 and rlt.rlt_plan_prefill([0, 0], group).num_items == 0
+    with pytest.raises(rlt.RltError):
+        rlt.rlt_plan_prefill([5, -1], group)
+    with pytest.raises(rlt.RltError):
+        rlt.rlt_plan_prefill([1 << 30, 1 << 30], group)
+    with pytest.raises(rlt.RltError):
+        rlt.rlt_plan_prefill([5], 0)
+    sizes = np.zeros(2, np.int32)
+    sl = np.array(lens, np.int32)
+    items = np.zeros((1, 4), np.int32)
+    p = lambda a: a.ctypes.data_as(ctypes.c_void_p)              # noqa: E731
+    assert lib.rlt_plan_prefill(p(sl), len(lens), group, p(items), 1, p(sizes)) == RANGE
+    assert sizes.tolist() == [len(want), sum(lens)]
+
+
 def test_reference_number_format():
     """The reference's e4m3 against torch's cast, and its row exponents at the edges."""
     import torch
