@@ -140,8 +140,8 @@ def _check(status: int, where: str):
 
 def _stream(stream):
     import torch
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:                           # (the raw handle: current_stream() builds a Stream object a call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -636,19 +636,14 @@ class KV8Pool:
 
 
 def _same_device(*tensors):
-    """The device of these tensors (None entries aside); they must share it, and it must be the current one:
+    """The index of these tensors' device (None entries aside); they must share it, and it must be the current one:
     the library launches on the current device."""
     import torch
-    found = None
+    found = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            continue
-        if found is None:
-            found = t.device
-        elif t.device != found:
-            raise ValueError(f"tensors on {found} and {t.device} in one call")
-    if found is not None and found.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {found}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t is not None and t.get_device() != found:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{found}: "
+                             "all tensors of a call must be on the current device")
     return found
 
 
@@ -669,20 +664,23 @@ def _token_rows(t, heads, D, n, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    if tuple(t.shape) != (n, heads, D):
+    if t.shape != (n, heads, D):
         raise ValueError(f"{name} must be [tokens][heads][head_dim] = {(n, heads, D)}, got {tuple(t.shape)}")
-    if n > 0 and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+    stride = t.stride()
+    if n > 0 and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * D)
+    return t.data_ptr(), (stride[0] if n > 1 else heads * D)
 
 
 def _ptr(t, dtype, name, shape=None):
     """Device address of a contiguous tensor of this type and shape, or 0 for None."""
     if t is None:
         return 0
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _dev(t, dtype, name).value or 0
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _dev(t, dtype, name)                                    # says what is wrong
+    return t.data_ptr()
 
 
 def rlt_kv8_append_rope(pool: KV8Pool, bank: int, k_new, v_new, positions, out_loc, rot_dim: int, rope_base: float,

@@ -123,7 +123,16 @@ RLT_API rlt_status rlt_kv8_append_rope(const rlt_kv8_pool *pool, int32_t bank, c
     p.head_dim = pool->head_dim;
     p.rot_dim = rot_dim;
     p.batch = batch;
-    rlt::rope_frequencies(rot_dim, rope_base, p.freq);
+    // the frequencies depend on (rot_dim, rope_base) alone, a model's constants: each host thread keeps
+    // its last ones (up to 64 powers are a few microseconds of a step's launch)
+    static thread_local struct { int32_t rot = -1; double base = 0.0; uint64_t freq[64]; } last;
+    if (last.rot != rot_dim || last.base != rope_base) {
+        rlt::rope_frequencies(rot_dim, rope_base, last.freq);
+        last.rot = rot_dim;
+        last.base = rope_base;
+    }
+    for (int i = 0; i < rot_dim / 2; ++i)
+        p.freq[i] = last.freq[i];
     return from_cuda(rlt::launch_kv8_append(p, static_cast<cudaStream_t>(stream)));
 }
 

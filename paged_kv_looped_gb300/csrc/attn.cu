@@ -70,36 +70,6 @@ __device__ __forceinline__ void load_frag_global(const uint16_t *src, float (&f)
     load_frag<DPL>(reinterpret_cast<const unsigned char *>(src), f);
 }
 
-// Pairs of fp32 in one 64-bit register: Blackwell's packed f32x2 FMA / MUL do two
-// lanes' worth of work per instruction (each half rounded as its own fmaf / fmul).
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ float2 f2_unpack(uint64_t v)
-{
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-    return make_float2(lo, hi);
-}
-
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // A tile row's DPL bf16 dims of this lane as DPL/2 fp32 pairs (bf16 -> fp32 is exact).
 template <int DPL>
 __device__ __forceinline__ void load_frag2(const unsigned char *src, uint64_t (&f)[DPL / 2])

@@ -19,101 +19,305 @@
 namespace rlt {
 namespace {
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
+constexpr int kSpreadWarps = 152 * 16;       // warps below which tokens are split by heads
 
-// cos and sin of `turns` / 2^64 turns.  x is off by at most 2^-33 turns and its fp32 rounding; the
-// polynomials' first dropped terms are below 2e-9 and 2e-10 for |x| <= pi/4.
+// cos and sin of `turns` / 2^64 turns, to a little over half an ulp: the angle x + dx in two parts (dx: what
+// the 24 bits of x leave of it), the polynomials' small terms added last.  Their first dropped terms
+// are below 2e-9 and 2e-10 for |x| <= pi/4.  Fewer keys are then held one e4m3 step off the exact rotation's
+// than with plain fp32 products of correctly rounded cosines.
 __device__ __forceinline__ void turn_cos_sin(uint64_t turns, float &c, float &s)
 {
+    constexpr float kUnit = 6.283185307179586f / 8589934592.f;            // 2 pi / 2^33
+    constexpr float kUnitLo = (float)(6.283185307179586 / 8589934592. - (double)kUnit);
     const uint32_t quadrant = (uint32_t)((turns + (1ull << 61)) >> 62);
     const int32_t rest = (int32_t)((int64_t)(turns - ((uint64_t)quadrant << 62)) >> 31);
-    const float x = (float)rest * (6.283185307179586f / 8589934592.f);   // 2 pi / 2^33
-    const float y = x * x;
-    const float sp = fmaf(fmaf(fmaf(fmaf(y, 1.f / 362880.f, -1.f / 5040.f), y, 1.f / 120.f), y, -1.f / 6.f), y * x, x);
-    const float cp = fmaf(
-        fmaf(fmaf(fmaf(fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), y, -1.f / 720.f), y, 1.f / 24.f), y, -0.5f), y, 1.f);
+    const float hi = (float)(rest & ~127), lo = (float)(rest & 127);      // hi: 24 bits, exact
+    const float x = hi * kUnit;
+    const float dx = fmaf(hi, kUnit, -x) + fmaf(hi, kUnitLo, lo * kUnit);
+    const float y = x * x, dy = fmaf(x, x, -y);
+    const float ps = fmaf(fmaf(fmaf(y, 1.f / 362880.f, -1.f / 5040.f), y, 1.f / 120.f), y, -1.f / 6.f) * (y * x);
+    const float pc = fmaf(fmaf(fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), y, -1.f / 720.f), y, 1.f / 24.f) * y;
+    const float w = fmaf(y, -0.5f, 1.f), dw = (1.f - w) - 0.5f * y;       // 1 - y/2 and what its rounding left
+    const float sp = x + (ps + fmaf(dx, -0.5f * y, dx));
+    const float cp = w + (dw + fmaf(pc, y, -fmaf(dx, x, 0.5f * dy)));
     const float cc = (quadrant & 1u) ? sp : cp, ss = (quadrant & 1u) ? cp : sp;
     c = ((quadrant + 1u) & 2u) ? -cc : cc;
     s = (quadrant & 2u) ? -ss : ss;
 }
 
-// One warp per row (a head of q, k or v of one token).
-__global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_kernel(const Kv8AppendParams p)
+// Where row h of a token (its query heads, then its key heads, then its value heads) comes from.
+struct RowAt {
+    const uint16_t *src;
+    int kind, g;                                 // 0 query, 1 key, 2 value; head
+};
+
+__device__ __forceinline__ RowAt row_at(const Kv8AppendParams &p, int64_t i, int h, int D)
 {
-    __shared__ float rows[kAppendWarps][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int D = p.head_dim, half = p.rot_dim / 2;
+    const int kind = h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2;
+    const int g = kind == 0 ? h : h - p.num_q_heads - (kind - 1) * p.num_kv_heads;
+    const uint16_t *src = kind == 0   ? p.q + i * p.q_stride
+                          : kind == 1 ? p.k_new + i * p.k_stride
+                                      : p.v_new + i * p.v_stride;
+    return {src + (int64_t)g * D, kind, g};
+}
+
+// The token's slot, or -1 where nothing is written for it; a slot past the pool is recorded once.
+__device__ __forceinline__ int64_t token_slot(const Kv8AppendParams &p, int64_t i, bool report)
+{
+    const int64_t slot = p.out_loc[i];
+    if (slot < p.num_slots)
+        return slot < 0 ? -1 : slot;
+    if (report)
+        record_error(p.err, RLT_DEVERR_BAD_SLOT);
+    return -1;
+}
+
+__device__ __forceinline__ void count_written(const Kv8AppendParams &p, int64_t i)
+{
+    const int32_t r = p.request[i];
+    if (r >= 0 && r < p.batch)
+        atomicMax(&p.written[r], (int32_t)min(p.positions[i] + 1, (int64_t)INT32_MAX));
+    else
+        record_error(p.err, RLT_DEVERR_BAD_SLOT);
+}
+
+// 16 values of a row from one 16-byte chunk pair: fp32, and the largest magnitude's bf16 bits.
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8])
+{
+    f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+    f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ uint32_t amax2(const uint4 &w)
+{
+    return __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8], float by)
+{
+    return make_uint4(cvt_bf16x2(f[0] * by, f[1] * by), cvt_bf16x2(f[2] * by, f[3] * by),
+                      cvt_bf16x2(f[4] * by, f[5] * by), cvt_bf16x2(f[6] * by, f[7] * by));
+}
+
+// Rotations whose halves are whole 16-byte chunks (rot_dim a multiple of 16; so is head_dim).  A lane holds the
+// two chunks of a row that turn into each other (or two neighbouring chunks behind rot_dim) and D / 16
+// lanes a row, so a row needs no exchange but its largest magnitude.  A warp stays with one token: its
+// angles are computed once and used for every head; the rows of kBatch rounds are loaded before
+// the first is worked on.  Bound by memory: 2 (hq + 2 hkv) D bytes in, as many out, and the cache.
+constexpr int kBatch = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(const Kv8AppendParams p, int splits)
+{
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int64_t i = w / splits;
+    if (i >= p.n_tokens)
+        return;
+    const int part = (int)(w - i * splits);
+    const int64_t slot = token_slot(p, i, part == 0 && lane == 0);
+    if (slot < 0)
+        return;
+    const int t = lane % kLanes, r0 = part * kRows + lane / kLanes, step = splits * kRows;
+    const int turned = p.rot_dim / 16;
+    const bool turns = t < turned;
+    const int ca = turns ? t : 2 * t, cb = turns ? t + turned : 2 * t + 1;   // this lane's chunks
     const int heads = p.num_q_heads + 2 * p.num_kv_heads;
-    const int64_t total = (int64_t)p.n_tokens * heads;
-    float *row = rows[warp];
-    for (int64_t w = (int64_t)blockIdx.x * kAppendWarps + warp; w < total; w += (int64_t)gridDim.x * kAppendWarps) {
-        const int64_t i = w / heads;
-        const int h = (int)(w - i * heads);
-        const int64_t slot = p.out_loc[i];
-        if (slot < 0)
-            continue;                            // no token for this entry
-        if (slot >= p.num_slots) {
-            if (h == 0 && lane == 0)
-                record_error(p.err, RLT_DEVERR_BAD_SLOT);
-            continue;
-        }
-        const int kind = h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2;
-        const int g = kind == 0 ? h : h - p.num_q_heads - (kind - 1) * p.num_kv_heads;
-        const uint16_t *src = kind == 0   ? p.q + i * p.q_stride + (int64_t)g * D
-                              : kind == 1 ? p.k_new + i * p.k_stride + (int64_t)g * D
-                                          : p.v_new + i * p.v_stride + (int64_t)g * D;
-        uint32_t amax = 0u;
-        __syncwarp();
-        for (int d = lane; d < D; d += 32) {
-            const uint32_t b = src[d];
-            amax = max(amax, b & 0x7fffu);
-            row[d] = __uint_as_float(b << 16);
-        }
-        amax = __reduce_max_sync(kFullMask, amax);
-        __syncwarp();
-        const uint64_t pos = kind < 2 && half > 0 ? (uint64_t)p.positions[i] : 0ull;
-        if (kind < 2) {
-            for (int j = lane; j < half; j += 32) {
-                float c, s;
-                turn_cos_sin(pos * p.freq[j], c, s);
-                const float a = row[j], b = row[j + half];
-                row[j] = fmaf(a, c, -(b * s));
-                row[j + half] = fmaf(b, c, a * s);
-            }
-            __syncwarp();
-        }
-        if (kind == 0) {
-            for (int d = lane * 2; d < D; d += 64)
-                reinterpret_cast<uint32_t *>(p.q_out)[((i * p.num_q_heads + g) * D + d) / 2] =
-                    cvt_bf16x2(row[d], row[d + 1]);
-            continue;
-        }
-        const uint32_t byte = row_exponent(amax);
-        const float scale = exp_scale(byte), inv = exp_inverse(byte);
-        const int64_t page = slot / p.page_size;
-        const int64_t at = (page * p.num_kv_heads + g) * p.page_size + (slot - page * p.page_size);
-        uint8_t *dst = (kind == 1 ? p.k_bank : p.v_bank) + at * D;
-        uint16_t *held = kind == 1 ? p.k_out : p.v_out;
-        for (int d = lane * 2; d < D; d += 64) {
-            const uint32_t x8 = e4m3x2(row[d] * inv, row[d + 1] * inv);
-            *reinterpret_cast<uint16_t *>(dst + d) = (uint16_t)x8;
-            if (held != nullptr) {
-                const float2 f = f32x2_of_f16(f16x2_of_e4m3(x8));
-                reinterpret_cast<uint32_t *>(held)[((i * p.num_kv_heads + g) * D + d) / 2] =
-                    cvt_bf16x2(f.x * scale, f.y * scale);
+
+    float c[8], s[8];
+    const uint64_t pos = turns ? (uint64_t)p.positions[i] : 0ull;
+    bool angles = false;
+    const int64_t page = slot / p.page_size;
+    const int64_t at0 = page * p.num_kv_heads * p.page_size + (slot - page * p.page_size);
+    for (int r = r0; r - r0 < heads - part * kRows; r += step * kBatch) {   // (uniform over the warp)
+        uint4 a[kBatch], b[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = r + u * step;
+            if (h < heads) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(row_at(p, i, h, D).src);
+                a[u] = __ldcs(src + ca);
+                b[u] = __ldcs(src + cb);
+            } else {
+                a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        if (lane == 0) {
-            (kind == 1 ? p.k_exp : p.v_exp)[at] = (uint8_t)byte;
-            if (kind == 1 && g == 0 && p.written != nullptr) {
-                const int32_t r = p.request[i];
-                if (r >= 0 && r < p.batch)
-                    atomicMax(&p.written[r], (int32_t)min(p.positions[i] + 1, (int64_t)INT32_MAX));
-                else
-                    record_error(p.err, RLT_DEVERR_BAD_SLOT);
+        if (!angles) {                           // while the first rows are on their way
+            angles = true;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                c[k] = s[k] = 0.f;
+                if (turns)
+                    turn_cos_sin(pos * p.freq[t * 8 + k], c[k], s[k]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = r + u * step;
+            uint32_t m2 = __vmaxu2(amax2(a[u]), amax2(b[u]));
+            uint32_t amax = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+                amax = max(amax, __shfl_xor_sync(kFullMask, amax, o));
+            if (h >= heads)
+                continue;
+            const RowAt row = row_at(p, i, h, D);
+            float fa[8], fb[8];
+            unpack8(a[u], fa);
+            unpack8(b[u], fb);
+            if (turns && row.kind < 2) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float x = fa[k], y = fb[k];
+                    fa[k] = fmaf(x, c[k], -(y * s[k]));
+                    fb[k] = fmaf(y, c[k], x * s[k]);
+                }
+            }
+            if (row.kind == 0) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + (i * p.num_q_heads + row.g) * D);
+                dst[ca] = pack8(fa, 1.f);
+                dst[cb] = pack8(fb, 1.f);
+                continue;
+            }
+            const uint32_t byte = row_exponent(amax);
+            const float scale = exp_scale(byte), inv = exp_inverse(byte);
+            const int64_t at = at0 + (int64_t)row.g * p.page_size;
+            uint2 *dst = reinterpret_cast<uint2 *>((row.kind == 1 ? p.k_bank : p.v_bank) + at * D);
+            uint16_t *held = row.kind == 1 ? p.k_out : p.v_out;
+            uint4 *hd = reinterpret_cast<uint4 *>(held + (held != nullptr ? (i * p.num_kv_heads + row.g) * D : 0));
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                float (&f)[8] = side == 0 ? fa : fb;
+                uint32_t x8[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x8[k] = e4m3x2(f[2 * k] * inv, f[2 * k + 1] * inv);
+                dst[side == 0 ? ca : cb] = make_uint2(x8[0] | (x8[1] << 16), x8[2] | (x8[3] << 16));
+                if (held != nullptr) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = f32x2_of_f16(f16x2_of_e4m3(x8[k]));
+                        f[2 * k] = v.x;
+                        f[2 * k + 1] = v.y;
+                    }
+                    hd[side == 0 ? ca : cb] = pack8(f, scale);
+                }
+            }
+            if (t == 0) {
+                (row.kind == 1 ? p.k_exp : p.v_exp)[at] = (uint8_t)byte;
+                if (row.kind == 1 && row.g == 0 && p.written != nullptr)
+                    count_written(p, i);
             }
         }
     }
+}
+
+// Any even rot_dim: a row passes through shared memory, where a lane finds the other member of its pairs.
+// A warp stays with one token; its angles (at most two pairs a lane) are computed once.
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(const Kv8AppendParams p, int splits)
+{
+    constexpr int kWords = D / 64;               // 32-bit words of a row that a lane loads
+    __shared__ float rows[kAppendWarps][D];
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int64_t i = w / splits;
+    if (i >= p.n_tokens)
+        return;
+    const int part = (int)(w - i * splits), half = p.rot_dim / 2;
+    const int64_t slot = token_slot(p, i, part == 0 && lane == 0);
+    if (slot < 0)
+        return;
+    float *row = rows[threadIdx.x >> 5];
+    const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+    float c[2], s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < half)
+            turn_cos_sin((uint64_t)p.positions[i] * p.freq[lane + 32 * k], c[k], s[k]);
+    const int64_t page = slot / p.page_size;
+    const int64_t at0 = page * p.num_kv_heads * p.page_size + (slot - page * p.page_size);
+    uint32_t next[kWords];
+    auto load = [&](int h) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(row_at(p, i, h, D).src) + lane * kWords;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            next[k] = src[k];
+    };
+    if (part < heads)
+        load(part);
+    for (int h = part; h < heads; h += splits) {
+        const RowAt r = row_at(p, i, h, D);
+        uint32_t amax = 0u;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const uint32_t x = next[k];
+            amax = max(amax, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
+            *reinterpret_cast<float2 *>(row + (lane * kWords + k) * 2) = make_float2(bf16_lo(x), bf16_hi(x));
+        }
+        if (h + splits < heads)
+            load(h + splits);
+        amax = __reduce_max_sync(kFullMask, amax);
+        __syncwarp();
+        if (r.kind < 2) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = lane + 32 * k;
+                if (j < half) {
+                    const float x = row[j], y = row[j + half];
+                    row[j] = fmaf(x, c[k], -(y * s[k]));
+                    row[j + half] = fmaf(y, c[k], x * s[k]);
+                }
+            }
+            __syncwarp();
+        }
+        const uint32_t byte = row_exponent(amax);
+        const float scale = exp_scale(byte), inv = exp_inverse(byte);
+        const int64_t at = at0 + (int64_t)r.g * p.page_size;
+        uint16_t *held = r.kind == 1 ? p.k_out : p.v_out;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const int d = (lane * kWords + k) * 2;
+            const float2 f = *reinterpret_cast<const float2 *>(row + d);
+            if (r.kind == 0) {
+                *reinterpret_cast<uint32_t *>(p.q_out + (i * p.num_q_heads + r.g) * D + d) = cvt_bf16x2(f.x, f.y);
+                continue;
+            }
+            const uint32_t x8 = e4m3x2(f.x * inv, f.y * inv);
+            *reinterpret_cast<uint16_t *>((r.kind == 1 ? p.k_bank : p.v_bank) + at * D + d) = (uint16_t)x8;
+            if (held != nullptr) {
+                const float2 v = f32x2_of_f16(f16x2_of_e4m3(x8));
+                *reinterpret_cast<uint32_t *>(held + (i * p.num_kv_heads + r.g) * D + d) =
+                    cvt_bf16x2(v.x * scale, v.y * scale);
+            }
+        }
+        if (r.kind != 0 && lane == 0) {
+            (r.kind == 1 ? p.k_exp : p.v_exp)[at] = (uint8_t)byte;
+            if (r.kind == 1 && r.g == 0 && p.written != nullptr)
+                count_written(p, i);
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_append_typed(const Kv8AppendParams &p, cudaStream_t stream)
+{
+    const int heads = p.num_q_heads + 2 * p.num_kv_heads;
+    const bool chunks = p.rot_dim % 16 == 0;
+    const int rounds = chunks ? (heads * (D / 16) + 31) / 32 : heads;
+    // Warps per token: few tokens are spread over the SMs, row by row; many keep one warp each, whose
+    // angles then serve all heads.
+    const int64_t want = kSpreadWarps / (p.n_tokens > 0 ? p.n_tokens : 1);
+    const int splits = (int)(want < 1 ? 1 : want < rounds ? want : rounds);
+    const int64_t blocks = ((int64_t)p.n_tokens * splits + kAppendWarps - 1) / kAppendWarps;
+    if (chunks)
+        kv8_append_chunks_kernel<D><<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(p, splits);
+    else
+        kv8_append_pairs_kernel<D><<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(p, splits);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -129,12 +333,7 @@ void rope_frequencies(int rot_dim, double base, uint64_t *freq)
 
 cudaError_t launch_kv8_append(const Kv8AppendParams &p, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)p.n_tokens * (p.num_q_heads + 2 * p.num_kv_heads);
-    int64_t blocks = (rows + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > (1 << 20))
-        blocks = 1 << 20;
-    kv8_append_kernel<<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.head_dim == 128 ? launch_append_typed<128>(p, stream) : launch_append_typed<64>(p, stream);
 }
 
 }  // namespace rlt

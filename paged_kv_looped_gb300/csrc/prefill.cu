@@ -36,7 +36,10 @@ namespace {
 
 constexpr int kTile = 128;                   // query rows, keys of a tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 10 * 32;
+constexpr int kThreads = 12 * 32;            // warps 10 and 11 only fill the third warpgroup
+// Registers a thread: 168 at launch (384 threads); the softmax warpgroups take up what the third one
+// gives back: 2 * 208 + 88 = 3 * 168.
+constexpr int kRegsSoftmax = 208, kRegsRest = 88;
 constexpr float kRescaleThreshold = 8.f;     // log2 units
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kItemFields = 4;               // first row of the sequence, its length, first query of the item, 0
@@ -122,127 +125,131 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tslot;
     bool ok = true;
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------- copies
-        // Ring order K0, V0, K1, V1, ...; rows behind the last one of the array read as zeros.
-        if (lane == 0) {
-            tc::prefetch_tmap(&qmap);
-            tc::prefetch_tmap(&kmap);
-            tc::prefetch_tmap(&vmap);
-        }
-        pdl_wait();
-        int issued = 0;
-        auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == kLoadWarp) {
+            // ---------------------------------------------------------- copies
+            // Ring order K0, V0, K1, V1, ...; rows behind the last one of the array read as zeros.
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, C::kTileBytes);
-                for (int b = 0; b < kBlocks; ++b)
-                    tma_load_3d(dst + b * C::kBlock, map, b * 64, head, row, bar);
+                tc::prefetch_tmap(&qmap);
+                tc::prefetch_tmap(&kmap);
+                tc::prefetch_tmap(&vmap);
             }
-        };
-        for (int i = 0; ok && i < 2 * n; ++i) {
-            if (i < 2 && (i == 0 || n1 > 0))
-                load(base + i * C::kTileBytes, &qmap, head0 + i * head_step, row0 + q0 + i * tok_step,
-                     &bars[C::kQFull + i]);
-            const int st = i % C::kStages;
-            if (i >= C::kStages && !(ok = warp_wait(&bars[C::kFree + st], ((i / C::kStages) - 1) & 1u, abort_flag)))
-                break;
-            load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head, row0 + (i >> 1) * kTile,
-                 &bars[C::kFull + st]);
-            issued = i + 1;
-        }
-        if (!ok)
-            *abort_flag = 1;
-        // every copy has landed before the CTA gives up its memory (bounded; on the normal path
-        // the products have waited for all of them)
-        if (lane == 0) {
-            for (int i = max(0, issued - C::kStages); i < issued; ++i)
-                mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
-            for (int i = 0; i < (n1 > 0 ? 2 : 1); ++i)
-                mbar_wait(&bars[C::kQFull + i], 0);
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------- products
-        // Issue order S0 S1 | PV0 S0' PV1 S1' | ...: MMAs of one thread run in issue order, so S of the
-        // next key tile may overwrite the P that the PV before it reads.
-        constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
-        constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
-        const uint32_t qa = smem_u32(base), ring = smem_u32(base + C::kRingOff);
-        auto wait_slot = [&](int i) -> bool {
-            return warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag);
-        };
-        auto issue_s = [&](int s, int j) {
-            if (lane == 0) {
-                const uint32_t a = qa + s * C::kTileBytes, b = ring + (2 * j) % C::kStages * C::kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc::mma_bf16(tmem + kColS + s * kTile,
-                                 tc::smem_desc(a + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024),
-                                 tc::smem_desc(b + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
-                tc::mma_commit(&bars[C::kSFull + s]);
-            }
-        };
-        auto issue_pv = [&](int s, int j) {
-            if (lane == 0) {
-                const uint32_t b = ring + (2 * j + 1) % C::kStages * C::kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc::mma_bf16_ta(tmem + kColO + s * kTile, tmem + kColS + s * kTile + kk * 8,
-                                    tc::smem_desc(b + kk * 2048, C::kBlock, 1024), id_o, j > 0 || kk > 0);
-                tc::mma_commit(&bars[C::kPvDone + s]);
-            }
-        };
-        auto release = [&](int i) {
-            if (lane == 0)
-                tc::mma_commit(&bars[C::kFree + i % C::kStages]);
-        };
-        int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0};
-        ok = wait_slot(0);
-        for (int s = 0; ok && s < 2; ++s) {
-            if ((s == 0 ? n0 : n1) == 0)
-                continue;
-            if (!(ok = warp_wait(&bars[C::kQFull + s], 0, abort_flag)))
-                break;
-            issue_s(s, 0);
-            s_issued[s] = 1;
-        }
-        if (ok)
-            release(0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (!(ok = wait_slot(2 * j + 1)) || (j + 1 < n && !(ok = wait_slot(2 * j + 2))))
-                break;
-            for (int s = 0; s < 2; ++s) {
-                const int ns = s == 0 ? n0 : n1;
-                if (j < ns) {
-                    if (!(ok = warp_wait(&bars[C::kPFull + s], j & 1u, abort_flag)))
-                        break;
-                    tc::fence_after_sync();
-                    issue_pv(s, j);
-                    pv_issued[s] = j + 1;
+            pdl_wait();
+            int issued = 0;
+            auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, C::kTileBytes);
+                    for (int b = 0; b < kBlocks; ++b)
+                        tma_load_3d(dst + b * C::kBlock, map, b * 64, head, row, bar);
                 }
-                if (j + 1 < ns) {
-                    issue_s(s, j + 1);
-                    s_issued[s] = j + 2;
-                }
+            };
+            for (int i = 0; ok && i < 2 * n; ++i) {
+                if (i < 2 && (i == 0 || n1 > 0))
+                    load(base + i * C::kTileBytes, &qmap, head0 + i * head_step, row0 + q0 + i * tok_step,
+                         &bars[C::kQFull + i]);
+                const int st = i % C::kStages;
+                if (i >= C::kStages && !(ok = warp_wait(&bars[C::kFree + st], ((i / C::kStages) - 1) & 1u, abort_flag)))
+                    break;
+                load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head, row0 + (i >> 1) * kTile,
+                     &bars[C::kFull + st]);
+                issued = i + 1;
             }
             if (!ok)
-                break;
-            release(2 * j + 1);
-            if (j + 1 < n)
-                release(2 * j + 2);
-        }
-        if (!ok)
-            *abort_flag = 1;
-        // every issued MMA is complete before the CTA gives up its memory (bounded)
-        if (lane == 0) {
-            for (int s = 0; s < 2; ++s) {
-                if (pv_issued[s] > 0)
-                    mbar_wait(&bars[C::kPvDone + s], (pv_issued[s] - 1) & 1u);
-                if (s_issued[s] > pv_issued[s])
-                    mbar_wait(&bars[C::kSFull + s], (s_issued[s] - 1) & 1u);
+                *abort_flag = 1;
+            // every copy has landed before the CTA gives up its memory (bounded; on the normal path
+            // the products have waited for all of them)
+            if (lane == 0) {
+                for (int i = max(0, issued - C::kStages); i < issued; ++i)
+                    mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
+                for (int i = 0; i < (n1 > 0 ? 2 : 1); ++i)
+                    mbar_wait(&bars[C::kQFull + i], 0);
             }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------- products
+            // Issue order S0 S1 | PV0 S0' PV1 S1' | ...: MMAs of one thread run in issue order, so S of the
+            // next key tile may overwrite the P that the PV before it reads.
+            constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
+            constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
+            const uint32_t qa = smem_u32(base), ring = smem_u32(base + C::kRingOff);
+            auto wait_slot = [&](int i) -> bool {
+                return warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag);
+            };
+            auto issue_s = [&](int s, int j) {
+                if (lane == 0) {
+                    const uint32_t a = qa + s * C::kTileBytes, b = ring + (2 * j) % C::kStages * C::kTileBytes;
+    #pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc::mma_bf16(tmem + kColS + s * kTile,
+                                     tc::smem_desc(a + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024),
+                                     tc::smem_desc(b + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
+                    tc::mma_commit(&bars[C::kSFull + s]);
+                }
+            };
+            auto issue_pv = [&](int s, int j) {
+                if (lane == 0) {
+                    const uint32_t b = ring + (2 * j + 1) % C::kStages * C::kTileBytes;
+    #pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        tc::mma_bf16_ta(tmem + kColO + s * kTile, tmem + kColS + s * kTile + kk * 8,
+                                        tc::smem_desc(b + kk * 2048, C::kBlock, 1024), id_o, j > 0 || kk > 0);
+                    tc::mma_commit(&bars[C::kPvDone + s]);
+                }
+            };
+            auto release = [&](int i) {
+                if (lane == 0)
+                    tc::mma_commit(&bars[C::kFree + i % C::kStages]);
+            };
+            int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0};
+            ok = wait_slot(0);
+            for (int s = 0; ok && s < 2; ++s) {
+                if ((s == 0 ? n0 : n1) == 0)
+                    continue;
+                if (!(ok = warp_wait(&bars[C::kQFull + s], 0, abort_flag)))
+                    break;
+                issue_s(s, 0);
+                s_issued[s] = 1;
+            }
+            if (ok)
+                release(0);
+            for (int j = 0; ok && j < n; ++j) {
+                if (!(ok = wait_slot(2 * j + 1)) || (j + 1 < n && !(ok = wait_slot(2 * j + 2))))
+                    break;
+                for (int s = 0; s < 2; ++s) {
+                    const int ns = s == 0 ? n0 : n1;
+                    if (j < ns) {
+                        if (!(ok = warp_wait(&bars[C::kPFull + s], j & 1u, abort_flag)))
+                            break;
+                        tc::fence_after_sync();
+                        issue_pv(s, j);
+                        pv_issued[s] = j + 1;
+                    }
+                    if (j + 1 < ns) {
+                        issue_s(s, j + 1);
+                        s_issued[s] = j + 2;
+                    }
+                }
+                if (!ok)
+                    break;
+                release(2 * j + 1);
+                if (j + 1 < n)
+                    release(2 * j + 2);
+            }
+            if (!ok)
+                *abort_flag = 1;
+            // every issued MMA is complete before the CTA gives up its memory (bounded)
+            if (lane == 0) {
+                for (int s = 0; s < 2; ++s) {
+                    if (pv_issued[s] > 0)
+                        mbar_wait(&bars[C::kPvDone + s], (pv_issued[s] - 1) & 1u);
+                    if (s_issued[s] > pv_issued[s])
+                        mbar_wait(&bars[C::kSFull + s], (s_issued[s] - 1) & 1u);
+                }
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2, quarter = warp & 3;
         const int ns = s == 0 ? n0 : n1;
@@ -269,24 +276,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async();
             }
-            float v[kTile];
-            {
-                float (&v0)[64] = *reinterpret_cast<float (*)[64]>(&v[0]);
-                float (&v1)[64] = *reinterpret_cast<float (*)[64]>(&v[64]);
-                tc::tmem_ld<64>(t_s, v0);
-                tc::tmem_ld<64>(t_s + 64, v1);
-            }
-            if (j == ns - 1) {                   // the diagonal: keys behind the query
-                const int last = q_tok - j * kTile;
+            // The row's scores, 32 columns at a time: the next load is under way while the maximum of
+            // the columns that have landed is taken (four chains).
+            float v[4][32];
+            float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+            const int last = j == ns - 1 ? q_tok - j * kTile : kTile;   // keys behind the query: the diagonal
+            tc::tmem_ld32_nowait(t_s, v[0]);
 #pragma unroll
-                for (int i = 0; i < kTile; ++i)
-                    v[i] = i <= last ? v[i] : -CUDART_INF_F;
-            }
-            float mx = -CUDART_INF_F;
+            for (int c = 0; c < 4; ++c) {
+                tc::tmem_wait_ld(v[c]);
+                if (c < 3)
+                    tc::tmem_ld32_nowait(t_s + (c + 1) * 32, v[c + 1]);
+                if (last < kTile - 1) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-                mx = fmaxf(mx, v[i]);
-            mx *= p.qscale;
+                    for (int i = 0; i < 32; ++i)
+                        v[c][i] = c * 32 + i <= last ? v[c][i] : -CUDART_INF_F;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx4[k] = fmaxf(fmaxf(mx4[k], v[c][i + k]), v[c][i + 4 + k]);
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
             const bool up = mx > m_ref + kRescaleThreshold;
             const float m_next = up ? mx : m_ref;
             const float scale_o = m_next == -CUDART_INF_F || m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(&bars[C::kPvDone + s], (j - 1) & 1u, abort_flag)))
                     break;
                 tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     float o[16];
                     uint32_t ow[16];
@@ -305,28 +317,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_st_nowait<16>(t_o + c * 16, ow);
                 }
             }
-            l_run *= scale_o;
             m_ref = m_next;
             const float m_sub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-            float lsum = 0.f;
+            const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = fast_exp2(fmaf(v[c * 32 + 2 * i], p.qscale, -m_sub));
-                    const float p1 = fast_exp2(fmaf(v[c * 32 + 2 * i + 1], p.qscale, -m_sub));
-                    lsum += p0 + p1;
-                    w[i] = cvt_bf16x2(p0, p1);
+                    const float2 x = f2_unpack(f2_fma(f2_pack(v[c][2 * i], v[c][2 * i + 1]), sc2, off2));
+                    v[c][2 * i] = fast_exp2(x.x);
+                    v[c][2 * i + 1] = fast_exp2(x.y);
+                    w[i] = cvt_bf16x2(v[c][2 * i], v[c][2 * i + 1]);
                 }
                 tc::tmem_st_nowait<16>(t_s + c * 16, w);
             }
             tc::tmem_wait_st();
-            l_run += lsum;
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&bars[C::kPFull + s]);
+            // the row's sum, off the path to the product
+            uint64_t sum2[4] = {f2_pack(l_run * scale_o, 0.f), 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(v[c][2 * i], v[c][2 * i + 1]));
+            const float2 sum = f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
+            l_run = sum.x + sum.y;
         }
         if (ok && ns > 0 && (ok = warp_wait(&bars[C::kPvDone + s], (ns - 1) & 1u, abort_flag))) {
             tc::fence_after_sync();
