@@ -52,7 +52,7 @@ struct PCfg {
     static constexpr int kRingOff = 2 * kTileBytes;              // behind the two Q tiles
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
     enum Bar { kQFull = 0, kFull = 2, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
-               kPvDone = kPFull + 2, kNumBars = kPvDone + 2 };
+               kPvDone = kPFull + 4, kNumBars = kPvDone + 2 };
     static constexpr int kFlagOff = kBarOff + kNumBars * 8;
     static constexpr int kSmem = kFlagOff + 16 + 1024;
 };
@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[C::kSFull + i], 1);
-            mbar_init(&bars[C::kPFull + i], 4);
+            mbar_init(&bars[C::kPFull + 2 * i], 4);
+            mbar_init(&bars[C::kPFull + 2 * i + 1], 4);
             mbar_init(&bars[C::kPvDone + i], 1);
         }
         *abort_flag = 0;
@@ -127,127 +128,144 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == kLoadWarp) {
+        if (warp == kLoadWarp && tc::elect_one()) {
             // ---------------------------------------------------------- copies
             // Ring order K0, V0, K1, V1, ...; rows behind the last one of the array read as zeros.
-            if (lane == 0) {
-                tc::prefetch_tmap(&qmap);
-                tc::prefetch_tmap(&kmap);
-                tc::prefetch_tmap(&vmap);
-            }
+            tc::prefetch_tmap(&qmap);
+            tc::prefetch_tmap(&kmap);
+            tc::prefetch_tmap(&vmap);
             pdl_wait();
-            int issued = 0;
             auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, C::kTileBytes);
-                    for (int b = 0; b < kBlocks; ++b)
-                        tma_load_3d(dst + b * C::kBlock, map, b * 64, head, row, bar);
-                }
+                mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+                    tma_load_3d(dst + b * C::kBlock, map, b * 64, head, row, bar);
             };
-            for (int i = 0; ok && i < 2 * n; ++i) {
-                if (i < 2 && (i == 0 || n1 > 0))
-                    load(base + i * C::kTileBytes, &qmap, head0 + i * head_step, row0 + q0 + i * tok_step,
-                         &bars[C::kQFull + i]);
-                const int st = i % C::kStages;
-                if (i >= C::kStages && !(ok = warp_wait(&bars[C::kFree + st], ((i / C::kStages) - 1) & 1u, abort_flag)))
+            int st = 0, issued = 0, queries = 0;
+            uint32_t parity = 1;                 // of the slot's previous release (none in the first round)
+            for (int i = 0; i < 2 * n; ++i) {
+                if (queries < 2 && (queries == 0 || n1 > 0)) {
+                    load(base + queries * C::kTileBytes, &qmap, head0 + queries * head_step,
+                         row0 + q0 + queries * tok_step, &bars[C::kQFull + queries]);
+                    ++queries;
+                }
+                if (i >= C::kStages && !(ok = mbar_wait_or_abort(&bars[C::kFree + st], parity, abort_flag)))
                     break;
-                load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head, row0 + (i >> 1) * kTile,
-                     &bars[C::kFull + st]);
+                load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head,
+                     row0 + (i >> 1) * kTile, &bars[C::kFull + st]);
                 issued = i + 1;
+                if (++st == C::kStages) {
+                    st = 0;
+                    parity ^= 1u;
+                }
             }
             if (!ok)
                 *abort_flag = 1;
             // every copy has landed before the CTA gives up its memory (bounded; on the normal path
             // the products have waited for all of them)
-            if (lane == 0) {
-                for (int i = max(0, issued - C::kStages); i < issued; ++i)
-                    mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
-                for (int i = 0; i < (n1 > 0 ? 2 : 1); ++i)
-                    mbar_wait(&bars[C::kQFull + i], 0);
-            }
-        } else if (warp == kMmaWarp) {
+            for (int i = max(0, issued - C::kStages); i < issued; ++i)
+                mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
+            for (int i = 0; i < queries; ++i)
+                mbar_wait(&bars[C::kQFull + i], 0);
+        } else if (warp == kMmaWarp && tc::elect_one()) {
             // ---------------------------------------------------------- products
             // Issue order S0 S1 | PV0 S0' PV1 S1' | ...: MMAs of one thread run in issue order, so S of the
-            // next key tile may overwrite the P that the PV before it reads.
+            // next key tile may overwrite the P that the PV before it reads.  An MMA keeps the tensor pipe 64
+            // clocks, so its issue has to take less: the descriptors are the tile's plus constants.
             constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
             constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
-            const uint32_t qa = smem_u32(base), ring = smem_u32(base + C::kRingOff);
-            auto wait_slot = [&](int i) -> bool {
-                return warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag);
-            };
-            auto issue_s = [&](int s, int j) {
-                if (lane == 0) {
-                    const uint32_t a = qa + s * C::kTileBytes, b = ring + (2 * j) % C::kStages * C::kTileBytes;
-    #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc::mma_bf16(tmem + kColS + s * kTile,
-                                     tc::smem_desc(a + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024),
-                                     tc::smem_desc(b + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024), id_s, kk > 0);
-                    tc::mma_commit(&bars[C::kSFull + s]);
+            const uint64_t qd = tc::smem_desc(smem_u32(base), 16, 1024);
+            const uint64_t kd = tc::smem_desc(smem_u32(base + C::kRingOff), 16, 1024);
+            const uint64_t vd = tc::smem_desc(smem_u32(base + C::kRingOff), C::kBlock, 1024);
+            constexpr uint64_t kTileStep = C::kTileBytes >> 4;
+            auto issue_s = [&](int s, int slot) {
+                const uint64_t a = qd + s * kTileStep, b = kd + slot * kTileStep;
+                const uint32_t d = tmem + kColS + s * kTile;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    constexpr uint64_t kStep = C::kBlock >> 4;
+                    tc::mma_bf16(d, a + (kk >> 2) * kStep + (kk & 3) * 2, b + (kk >> 2) * kStep + (kk & 3) * 2, id_s,
+                                 kk > 0);
                 }
+                tc::mma_commit(&bars[C::kSFull + s]);
             };
-            auto issue_pv = [&](int s, int j) {
-                if (lane == 0) {
-                    const uint32_t b = ring + (2 * j + 1) % C::kStages * C::kTileBytes;
-    #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::mma_bf16_ta(tmem + kColO + s * kTile, tmem + kColS + s * kTile + kk * 8,
-                                        tc::smem_desc(b + kk * 2048, C::kBlock, 1024), id_o, j > 0 || kk > 0);
-                    tc::mma_commit(&bars[C::kPvDone + s]);
-                }
-            };
-            auto release = [&](int i) {
-                if (lane == 0)
-                    tc::mma_commit(&bars[C::kFree + i % C::kStages]);
+            auto issue_pv = [&](int s, int half, int slot, bool first) {      // 64 keys
+                const uint64_t b = vd + slot * kTileStep + half * (4 * 2048 >> 4);
+                const uint32_t d = tmem + kColO + s * kTile, a = tmem + kColS + s * kTile + half * 32;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_bf16_ta(d, a + kk * 8, b + kk * (2048 >> 4), id_o, kk > 0 || !first);
             };
             int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0};
-            ok = wait_slot(0);
-            for (int s = 0; ok && s < 2; ++s) {
-                if ((s == 0 ? n0 : n1) == 0)
+            // ring slot and parity of the next copy to be waited for
+            int st = 0;
+            uint32_t parity = 0;
+            auto wait_slot = [&](int &slot) -> bool {
+                slot = st;
+                if (!mbar_wait_or_abort(&bars[C::kFull + st], parity, abort_flag))
+                    return false;
+                if (++st == C::kStages) {
+                    st = 0;
+                    parity ^= 1u;
+                }
+                return true;
+            };
+            int k_slot = 0, v_slot = 0;
+            ok = wait_slot(k_slot);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (!ok || (s == 0 ? n0 : n1) == 0)
                     continue;
-                if (!(ok = warp_wait(&bars[C::kQFull + s], 0, abort_flag)))
-                    break;
-                issue_s(s, 0);
-                s_issued[s] = 1;
+                if ((ok = mbar_wait_or_abort(&bars[C::kQFull + s], 0, abort_flag))) {
+                    issue_s(s, k_slot);
+                    s_issued[s] = 1;
+                }
             }
             if (ok)
-                release(0);
+                tc::mma_commit(&bars[C::kFree + k_slot]);
             for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = wait_slot(2 * j + 1)) || (j + 1 < n && !(ok = wait_slot(2 * j + 2))))
+                if (!(ok = wait_slot(v_slot)) || (j + 1 < n && !(ok = wait_slot(k_slot))))
                     break;
+#pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const int ns = s == 0 ? n0 : n1;
-                    if (j < ns) {
-                        if (!(ok = warp_wait(&bars[C::kPFull + s], j & 1u, abort_flag)))
-                            break;
-                        tc::fence_after_sync();
-                        issue_pv(s, j);
-                        pv_issued[s] = j + 1;
-                    }
+                    if (!ok || j >= ns)
+                        continue;
+                    if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], j & 1u, abort_flag)))
+                        continue;
+                    tc::fence_after_sync();
+                    issue_pv(s, 0, v_slot, j == 0);
+                    ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], j & 1u, abort_flag);
+                    tc::fence_after_sync();
+                    if (ok)
+                        issue_pv(s, 1, v_slot, false);
+                    tc::mma_commit(&bars[C::kPvDone + s]);
+                    pv_issued[s] = j + 1;
+                    if (!ok)
+                        continue;
                     if (j + 1 < ns) {
-                        issue_s(s, j + 1);
+                        issue_s(s, k_slot);
                         s_issued[s] = j + 2;
                     }
                 }
                 if (!ok)
                     break;
-                release(2 * j + 1);
+                tc::mma_commit(&bars[C::kFree + v_slot]);
                 if (j + 1 < n)
-                    release(2 * j + 2);
+                    tc::mma_commit(&bars[C::kFree + k_slot]);
             }
             if (!ok)
                 *abort_flag = 1;
             // every issued MMA is complete before the CTA gives up its memory (bounded)
-            if (lane == 0) {
-                for (int s = 0; s < 2; ++s) {
-                    if (pv_issued[s] > 0)
-                        mbar_wait(&bars[C::kPvDone + s], (pv_issued[s] - 1) & 1u);
-                    if (s_issued[s] > pv_issued[s])
-                        mbar_wait(&bars[C::kSFull + s], (s_issued[s] - 1) & 1u);
-                }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (pv_issued[s] > 0)
+                    mbar_wait(&bars[C::kPvDone + s], (pv_issued[s] - 1) & 1u);
+                if (s_issued[s] > pv_issued[s])
+                    mbar_wait(&bars[C::kSFull + s], (s_issued[s] - 1) & 1u);
             }
-            __syncwarp();
         }
+        __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax
@@ -257,6 +275,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t t_s = t_lane + kColS + s * kTile, t_o = t_lane + kColO + s * kTile;
         float m_ref = -CUDART_INF_F, l_run = 0.f;
+        auto p_ready = [&](int half) {           // this warp's P of 64 keys is in tensor memory
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars[C::kPFull + 2 * s + half]);
+        };
         for (int j = 0; j < ns; ++j) {
             if (!(ok = warp_wait(&bars[C::kSFull + s], j & 1u, abort_flag)))
                 break;
@@ -276,76 +301,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async();
             }
-            // The row's scores, 32 columns at a time: the next load is under way while the maximum of
-            // the columns that have landed is taken (four chains).
             float v[4][32];
-            float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-            const int last = j == ns - 1 ? q_tok - j * kTile : kTile;   // keys behind the query: the diagonal
-            tc::tmem_ld32_nowait(t_s, v[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 4; ++c)
+                tc::tmem_ld32_nowait(t_s + c * 32, v[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
                 tc::tmem_wait_ld(v[c]);
-                if (c < 3)
-                    tc::tmem_ld32_nowait(t_s + (c + 1) * 32, v[c + 1]);
-                if (last < kTile - 1) {
+            if (j == ns - 1) {                   // the diagonal: keys behind the query
+                const int last = q_tok - j * kTile;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[c][i] = c * 32 + i <= last ? v[c][i] : -CUDART_INF_F;
+                for (int i = 0; i < kTile; ++i)
+                    v[i / 32][i % 32] = i <= last ? v[i / 32][i % 32] : -CUDART_INF_F;
+            }
+            // P = 2^(s - m) of 32 columns and their sum.  The first ones are made against the reference the row
+            // has, beside the row's maximum: it moves rarely, and then they are made again.
+            uint64_t sum2[2];
+            auto weights = [&](const float (&x)[32], uint32_t (&w)[16], float m) {
+                const float m_sub = m == -CUDART_INF_F ? 0.f : m;
+                const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
+                    const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+                    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+                    w[i] = cvt_bf16x2(p0, p1);
                 }
+            };
+            uint32_t w[16];
+            sum2[0] = sum2[1] = 0ull;
+            weights(v[0], w, m_ref);
+            float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int i = 0; i < 32; i += 8)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mx4[k] = fmaxf(fmaxf(mx4[k], v[c][i + k]), v[c][i + 4 + k]);
-            }
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
             const bool up = mx > m_ref + kRescaleThreshold;
-            const float m_next = up ? mx : m_ref;
-            const float scale_o = m_next == -CUDART_INF_F || m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
-            if (j > 0 && __any_sync(kFullMask, up)) {
-                if (!(ok = warp_wait(&bars[C::kPvDone + s], (j - 1) & 1u, abort_flag)))
-                    break;
-                tc::fence_after_sync();
+            if (__any_sync(kFullMask, up)) {
+                const float m_next = up ? mx : m_ref;
+                const float scale_o = m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
+                if (j > 0) {
+                    if (!(ok = warp_wait(&bars[C::kPvDone + s], (j - 1) & 1u, abort_flag)))
+                        break;
+                    tc::fence_after_sync();
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    float o[16];
-                    uint32_t ow[16];
-                    tc::tmem_ld<16>(t_o + c * 16, o);
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        uint32_t ow[16];
+                        tc::tmem_ld<16>(t_o + c * 16, o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        ow[i] = __float_as_uint(o[i] * scale_o);
-                    tc::tmem_st_nowait<16>(t_o + c * 16, ow);
+                        for (int i = 0; i < 16; ++i)
+                            ow[i] = __float_as_uint(o[i] * scale_o);
+                        tc::tmem_st_nowait<16>(t_o + c * 16, ow);
+                    }
                 }
+                l_run *= scale_o;
+                m_ref = m_next;
+                sum2[0] = sum2[1] = 0ull;
+                weights(v[0], w, m_ref);
             }
-            m_ref = m_next;
-            const float m_sub = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-            const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 x = f2_unpack(f2_fma(f2_pack(v[c][2 * i], v[c][2 * i + 1]), sc2, off2));
-                    v[c][2 * i] = fast_exp2(x.x);
-                    v[c][2 * i + 1] = fast_exp2(x.y);
-                    w[i] = cvt_bf16x2(v[c][2 * i], v[c][2 * i + 1]);
-                }
-                tc::tmem_st_nowait<16>(t_s + c * 16, w);
-            }
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars[C::kPFull + s]);
-            // the row's sum, off the path to the product
-            uint64_t sum2[4] = {f2_pack(l_run * scale_o, 0.f), 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(v[c][2 * i], v[c][2 * i + 1]));
-            const float2 sum = f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])));
-            l_run = sum.x + sum.y;
+            tc::tmem_st_nowait<16>(t_s, w);
+            weights(v[1], w, m_ref);
+            tc::tmem_st_nowait<16>(t_s + 16, w);
+            weights(v[2], w, m_ref);
+            p_ready(0);                          // the first 64 keys' weights
+            tc::tmem_st_nowait<16>(t_s + 32, w);
+            weights(v[3], w, m_ref);
+            tc::tmem_st_nowait<16>(t_s + 48, w);
+            p_ready(1);
+            const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
+            l_run += sum.x + sum.y;
         }
         if (ok && ns > 0 && (ok = warp_wait(&bars[C::kPvDone + s], (ns - 1) & 1u, abort_flag))) {
             tc::fence_after_sync();

@@ -74,6 +74,15 @@ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t k)
     return (row >> 3) * 1024u + (row & 7u) * 128u + chunk * 16u + (k & 7u) * 2u;
 }
 
+// True in one lane of a converged warp (always the same one).  The compiler knows a single lane runs
+// what depends on it, so the operands of TMA and MMA instructions stay in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
+
 // ----------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor (tcgen05): start address, leading and stride
 // byte offsets (all >> 4), descriptor version 1, 128-byte swizzle.
