@@ -16,7 +16,7 @@
 // a CTA (first copies, no overlap) and by their ragged last tiles.
 //
 // Roles: warps 0-3 / 4-7 softmax of tile 0 / 1 (a thread owns one row = one tensor-memory lane:
-// row maxima and sums need no exchange), warp 8 issues the MMAs, warp 9 the copies.  P (bf16)
+// row maxima and sums need no exchange), warp 8 / 9 the MMAs of tile 0 / 1, warp 10 the copies.  P (bf16)
 // is written over the S it came from.  The reference maximum of a row moves only when the running
 // maximum exceeds it by 2^8, so O is rescaled rarely, by the row's own thread.
 #include <cuda.h>
@@ -35,8 +35,8 @@ namespace rlt {
 namespace {
 
 constexpr int kTile = 128;                   // query rows, keys of a tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 12 * 32;            // warps 10 and 11 only fill the third warpgroup
+constexpr int kMmaWarp = 8, kLoadWarp = 10;  // MMA warps 8 and 9: one a tile
+constexpr int kThreads = 12 * 32;            // warp 11 only fills the third warpgroup
 // Registers a thread: 168 at launch (384 threads); the softmax warpgroups take up what the third one
 // gives back: 2 * 208 + 88 = 3 * 168.
 constexpr int kRegsSoftmax = 208, kRegsRest = 88;
@@ -70,6 +70,14 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
 {
     return __all_sync(kFullMask, mbar_wait_or_abort(bar, parity, abort));
+}
+
+// 2^x, kept in program order among volatile instructions.
+__device__ __forceinline__ float exp2_in_order(float x)
+{
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 template <int D>
@@ -108,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::kSFull; ++i)
-            mbar_init(&bars[i], 1);
+            mbar_init(&bars[i], i < C::kFree ? 1 : 2);   // a slot is free once both tiles' products have read it
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[C::kSFull + i], 1);
             mbar_init(&bars[C::kPFull + 2 * i], 4);
@@ -167,36 +175,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
             for (int i = 0; i < queries; ++i)
                 mbar_wait(&bars[C::kQFull + i], 0);
-        } else if (warp == kMmaWarp && tc::elect_one()) {
+        } else if (warp < kLoadWarp && tc::elect_one()) {
             // ---------------------------------------------------------- products
-            // Issue order S0 S1 | PV0 S0' PV1 S1' | ...: MMAs of one thread run in issue order, so S of the
-            // next key tile may overwrite the P that the PV before it reads.  An MMA keeps the tensor pipe 64
-            // clocks, so its issue has to take less: the descriptors are the tile's plus constants.
+            // One thread a tile, in the order S | PV S' | PV' S'' ...: MMAs of one thread run in issue order,
+            // so S of the next key tile may overwrite the P that the PV before it reads.  A wait costs a thread
+            // about 75 clocks and a full MMA queue holds it up; with a thread a tile neither delays the
+            // other tile's products (one thread for both measured 352 us where two take 322: 8192
+            // tokens, 32 heads).  An MMA keeps the tensor pipe 64 clocks, so its issue has to take
+            // less: the descriptors are the tile's plus constants.
+            const int s = warp - kMmaWarp;
+            const int ns = s == 0 ? n0 : n1;
             constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
             constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
-            const uint64_t qd = tc::smem_desc(smem_u32(base), 16, 1024);
+            constexpr uint64_t kTileStep = C::kTileBytes >> 4;
+            const uint64_t qd = tc::smem_desc(smem_u32(base), 16, 1024) + s * kTileStep;
             const uint64_t kd = tc::smem_desc(smem_u32(base + C::kRingOff), 16, 1024);
             const uint64_t vd = tc::smem_desc(smem_u32(base + C::kRingOff), C::kBlock, 1024);
-            constexpr uint64_t kTileStep = C::kTileBytes >> 4;
-            auto issue_s = [&](int s, int slot) {
-                const uint64_t a = qd + s * kTileStep, b = kd + slot * kTileStep;
-                const uint32_t d = tmem + kColS + s * kTile;
+            const uint32_t t_s = tmem + kColS + s * kTile, t_o = tmem + kColO + s * kTile;
+            auto issue_s = [&](int slot) {
+                const uint64_t b = kd + slot * kTileStep;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     constexpr uint64_t kStep = C::kBlock >> 4;
-                    tc::mma_bf16(d, a + (kk >> 2) * kStep + (kk & 3) * 2, b + (kk >> 2) * kStep + (kk & 3) * 2, id_s,
+                    tc::mma_bf16(t_s, qd + (kk >> 2) * kStep + (kk & 3) * 2, b + (kk >> 2) * kStep + (kk & 3) * 2, id_s,
                                  kk > 0);
                 }
                 tc::mma_commit(&bars[C::kSFull + s]);
             };
-            auto issue_pv = [&](int s, int half, int slot, bool first) {      // 64 keys
+            auto issue_pv = [&](int half, int slot, bool first) {             // 64 keys
                 const uint64_t b = vd + slot * kTileStep + half * (4 * 2048 >> 4);
-                const uint32_t d = tmem + kColO + s * kTile, a = tmem + kColS + s * kTile + half * 32;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_bf16_ta(d, a + kk * 8, b + kk * (2048 >> 4), id_o, kk > 0 || !first);
+                    tc::mma_bf16_ta(t_o, t_s + half * 32 + kk * 8, b + kk * (2048 >> 4), id_o, kk > 0 || !first);
             };
-            int s_issued[2] = {0, 0}, pv_issued[2] = {0, 0};
             // ring slot and parity of the next copy to be waited for
             int st = 0;
             uint32_t parity = 0;
@@ -210,60 +221,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            int k_slot = 0, v_slot = 0;
-            ok = wait_slot(k_slot);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (!ok || (s == 0 ? n0 : n1) == 0)
-                    continue;
-                if ((ok = mbar_wait_or_abort(&bars[C::kQFull + s], 0, abort_flag))) {
-                    issue_s(s, k_slot);
-                    s_issued[s] = 1;
+            // a tile without work on a copy lets it go at once
+            auto release = [&](int slot, bool used) {
+                if (used)
+                    tc::mma_commit(&bars[C::kFree + slot]);
+                else
+                    mbar_arrive(&bars[C::kFree + slot]);
+            };
+            int k_slot = 0, v_slot = 0, s_issued = 0, pv_issued = 0;
+            ok = wait_slot(k_slot) && (ns == 0 || mbar_wait_or_abort(&bars[C::kQFull + s], 0, abort_flag));
+            if (ok) {
+                if (ns > 0) {
+                    issue_s(k_slot);
+                    s_issued = 1;
                 }
+                release(k_slot, ns > 0);
             }
-            if (ok)
-                tc::mma_commit(&bars[C::kFree + k_slot]);
             for (int j = 0; ok && j < n; ++j) {
                 if (!(ok = wait_slot(v_slot)) || (j + 1 < n && !(ok = wait_slot(k_slot))))
                     break;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int ns = s == 0 ? n0 : n1;
-                    if (!ok || j >= ns)
-                        continue;
+                if (j < ns) {
                     if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], j & 1u, abort_flag)))
-                        continue;
+                        break;
                     tc::fence_after_sync();
-                    issue_pv(s, 0, v_slot, j == 0);
+                    issue_pv(0, v_slot, j == 0);
+                    pv_issued = j + 1;
                     ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], j & 1u, abort_flag);
                     tc::fence_after_sync();
                     if (ok)
-                        issue_pv(s, 1, v_slot, false);
+                        issue_pv(1, v_slot, false);
                     tc::mma_commit(&bars[C::kPvDone + s]);
-                    pv_issued[s] = j + 1;
                     if (!ok)
-                        continue;
+                        break;
                     if (j + 1 < ns) {
-                        issue_s(s, k_slot);
-                        s_issued[s] = j + 2;
+                        issue_s(k_slot);
+                        s_issued = j + 2;
                     }
                 }
-                if (!ok)
-                    break;
-                tc::mma_commit(&bars[C::kFree + v_slot]);
+                release(v_slot, j < ns);
                 if (j + 1 < n)
-                    tc::mma_commit(&bars[C::kFree + k_slot]);
+                    release(k_slot, j + 1 < ns);
             }
             if (!ok)
                 *abort_flag = 1;
             // every issued MMA is complete before the CTA gives up its memory (bounded)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (pv_issued[s] > 0)
-                    mbar_wait(&bars[C::kPvDone + s], (pv_issued[s] - 1) & 1u);
-                if (s_issued[s] > pv_issued[s])
-                    mbar_wait(&bars[C::kSFull + s], (s_issued[s] - 1) & 1u);
-            }
+            if (pv_issued > 0)
+                mbar_wait(&bars[C::kPvDone + s], (pv_issued - 1) & 1u);
+            if (s_issued > pv_issued)
+                mbar_wait(&bars[C::kSFull + s], (s_issued - 1) & 1u);
         }
         __syncwarp();
     } else {
@@ -314,23 +319,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kTile; ++i)
                     v[i / 32][i % 32] = i <= last ? v[i / 32][i % 32] : -CUDART_INF_F;
             }
-            // P = 2^(s - m) of 32 columns and their sum.  The first ones are made against the reference the row
-            // has, beside the row's maximum: it moves rarely, and then they are made again.
-            uint64_t sum2[2];
-            auto weights = [&](const float (&x)[32], uint32_t (&w)[16], float m) {
+            // P = 2^(s - m), 32 columns at a time.  The first ones are made against the reference the row has,
+            // beside the row's maximum: it moves rarely, and then they are made again.  The exponentials
+            // of the next columns are issued ahead of the conversions of the last ones: the unit
+            // that makes them (8 lanes a clock) is what a warp waits for.
+            auto raise = [&](const float (&x)[32], float (&y)[32], float m) {
                 const float m_sub = m == -CUDART_INF_F ? 0.f : m;
                 const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 y = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
-                    const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
-                    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
-                    w[i] = cvt_bf16x2(p0, p1);
+                    const float2 z = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
+                    y[2 * i] = exp2_in_order(z.x);
+                    y[2 * i + 1] = exp2_in_order(z.y);
                 }
             };
-            uint32_t w[16];
-            sum2[0] = sum2[1] = 0ull;
-            weights(v[0], w, m_ref);
+            uint64_t sum2[2] = {0ull, 0ull};
+            auto store = [&](const float (&y)[32], int c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[i] = cvt_bf16x2(y[2 * i], y[2 * i + 1]);
+                tc::tmem_st_nowait<16>(t_s + c * 16, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(y[2 * i], y[2 * i + 1]));
+            };
+            float y0[32];
+            raise(v[0], y0, m_ref);
             float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -361,17 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l_run *= scale_o;
                 m_ref = m_next;
-                sum2[0] = sum2[1] = 0ull;
-                weights(v[0], w, m_ref);
+                raise(v[0], y0, m_ref);
             }
-            tc::tmem_st_nowait<16>(t_s, w);
-            weights(v[1], w, m_ref);
-            tc::tmem_st_nowait<16>(t_s + 16, w);
-            weights(v[2], w, m_ref);
+            raise(v[1], v[1], m_ref);
+            store(y0, 0);
+            raise(v[2], v[2], m_ref);
+            store(v[1], 1);
             p_ready(0);                          // the first 64 keys' weights
-            tc::tmem_st_nowait<16>(t_s + 32, w);
-            weights(v[3], w, m_ref);
-            tc::tmem_st_nowait<16>(t_s + 48, w);
+            raise(v[3], v[3], m_ref);
+            store(v[2], 2);
+            store(v[3], 3);
             p_ready(1);
             const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
             l_run += sum.x + sum.y;
