@@ -51,10 +51,30 @@ struct PCfg {
     static constexpr int kTileBytes = D / 64 * kBlock;
     static constexpr int kRingOff = 2 * kTileBytes;              // behind the two Q tiles
     static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-    enum Bar { kQFull = 0, kFull = 2, kFree = kFull + kStages, kSFull = kFree + kStages, kPFull = kSFull + 2,
-               kPvDone = kPFull + 4, kNumBars = kPvDone + 2 };
-    static constexpr int kFlagOff = kBarOff + kNumBars * 8;
+    enum Bar {
+        kQFull = 0,                          // [tile] the item's Q landed
+        kQFree = kQFull + 2,                 // [tile] read by its last S
+        kFull = kQFree + 2,                  // [ring slot] K or V landed
+        kFree = kFull + kStages,             // [ring slot] read by both tiles' products
+        kSFull = kFree + kStages,            // [tile] S of a key tile written
+        kPFull = kSFull + 2,                 // [tile][64 keys] P written by the tile's 4 warps
+        kODone = kPFull + 4,                 // [tile] the item's last P V complete
+        kOFree = kODone + 2,                 // [tile] O read out by the tile's 4 warps
+        kWorkFull = kOFree + 2,              // [2] a work descriptor published
+        kWorkFree = kWorkFull + 2,           // [2] every role is done with it
+        kNext = kWorkFree + 2,               // the scheduler's answer landed
+        kNumBars = kNext + 1
+    };
+    static constexpr int kWorkOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;   // two Work
+    static constexpr int kNextOff = kWorkOff + 32;               // the scheduler's 16-byte answer
+    static constexpr int kBadOff = kNextOff + 16;                // [2 items][tile][4] rows with non-finite values
+    static constexpr int kFlagOff = kBadOff + 64;
     static constexpr int kSmem = kFlagOff + 16 + 1024;
+};
+
+// One work item: query rows q0.. of a sequence (rows row0 .. row0 + len - 1) for one unit of heads.
+struct Work {
+    int32_t row0, len, q0, unit;             // len 0: nothing to do; -1: no more work
 };
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
@@ -65,6 +85,33 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// Cluster launch control: asks the hardware scheduler for the block of this grid it would start next.  The
+// 16-byte answer lands in shared memory and completes 16 bytes of the barrier's transaction count.
+__device__ __forceinline__ void ask_for_block(void *answer, uint64_t *bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The block number of an answer, or -1 when the grid has no block left to start.
+__device__ __forceinline__ int answered_block(const void *answer)
+{
+    int32_t x, got;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.b32 %1, 1, 0, p;\n\t"
+        "mov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, h;\n\t}"
+        : "=r"(x), "=r"(got)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return got != 0 ? x : -1;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
@@ -80,6 +127,9 @@ __device__ __forceinline__ float exp2_in_order(float x)
     return r;
 }
 
+// Whether a word of two bf16 values holds an infinity or NaN, from the larger magnitude's bits.
+__device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0xffffu) >= 0x7f80u || bits >= 0x7f800000u; }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -91,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char *base =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + C::kBarOff);
+    volatile Work *works = reinterpret_cast<volatile Work *>(base + C::kWorkOff);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(base + C::kFlagOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + C::kFlagOff + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,33 +150,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = p.num_q_heads / p.num_kv_heads;
     const bool pair = G % 2 == 0;                // tile 1: the next head, else the next 128 tokens
     const int units = pair ? p.num_q_heads / 2 : p.num_q_heads;
-    const int item = blockIdx.x / units, unit = blockIdx.x - item * units;
-    const int32_t *it = p.items + (int64_t)item * kItemFields;
-    const int row0 = it[0], len = it[1], q0 = it[2];
-    if (row0 < 0 || len < 1 || len > p.num_rows - row0 || q0 < 0 || q0 >= len || q0 % kTile != 0) {
-        if (tid == 0)
-            record_error(p.err, RLT_DEVERR_BAD_LEN);   // a plan of other sequences
-        return;
-    }
-    const int head0 = pair ? 2 * unit : unit, kv_head = head0 / G;
     const int head_step = pair ? 1 : 0, tok_step = pair ? 0 : kTile;
-    // key tiles of each query tile: up to its last row's own key
-    const int n0 = q0 / kTile + 1;
-    const int n1 = q0 + tok_step < len ? n0 + tok_step / kTile : 0;
-    const int n = max(n0, n1);
 
     if (tid == 0) {
-        for (int i = 0; i < C::kSFull; ++i)
-            mbar_init(&bars[i], i < C::kFree ? 1 : 2);   // a slot is free once both tiles' products have read it
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[C::kSFull + i], 1);
-            mbar_init(&bars[C::kPFull + 2 * i], 4);
-            mbar_init(&bars[C::kPFull + 2 * i + 1], 4);
-            mbar_init(&bars[C::kPvDone + i], 1);
+        for (int i = 0; i < C::kNumBars; ++i) {
+            int count = 1;
+            if (i >= C::kFree && i < C::kSFull)
+                count = 2;                       // both tiles' MMA threads
+            else if ((i >= C::kPFull && i < C::kODone) || (i >= C::kOFree && i < C::kWorkFull))
+                count = 4;                       // the tile's softmax warps
+            else if (i >= C::kWorkFree && i < C::kNext)
+                count = 10;                      // two MMA threads, eight softmax warps
+            mbar_init(&bars[i], count);
         }
         *abort_flag = 0;
         mbar_init_fence();
     }
+    if (tid < 16)
+        reinterpret_cast<uint32_t *>(base + C::kBadOff)[tid] = 0u;
     if (warp == kMmaWarp)
         tc::tmem_alloc(tslot, kTmemCols);
     tc::fence_before_sync();
@@ -134,11 +176,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tslot;
     bool ok = true;
 
+    // Every role goes through the same works; key tiles of tile s: up to its last row's own key.
+    auto take = [&](int d, Work &w) {            // (the barrier has been waited for)
+        w.row0 = works[d & 1].row0;
+        w.len = works[d & 1].len;
+        w.q0 = works[d & 1].q0;
+        w.unit = works[d & 1].unit;
+    };
+    auto key_tiles = [&](const Work &w, int s) -> int {
+        return w.len <= w.q0 + s * tok_step ? 0 : w.q0 / kTile + 1 + s * (tok_step / kTile);
+    };
+
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         if (warp == kLoadWarp && tc::elect_one()) {
-            // ---------------------------------------------------------- copies
-            // Ring order K0, V0, K1, V1, ...; rows behind the last one of the array read as zeros.
+            // ------------------------------------------------- works and copies
+            // The CTA's own block first, then the ones the hardware scheduler hands over instead of starting
+            // them: the items keep their order, and a CTA's start is paid once.  The next work is asked
+            // for while this one's copies are issued.  Ring order K0, V0, K1, V1, ...; rows behind
+            // the last one of the array read as zeros.
             tc::prefetch_tmap(&qmap);
             tc::prefetch_tmap(&kmap);
             tc::prefetch_tmap(&vmap);
@@ -149,64 +205,114 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < kBlocks; ++b)
                     tma_load_3d(dst + b * C::kBlock, map, b * 64, head, row, bar);
             };
-            int st = 0, issued = 0, queries = 0;
+            int block = blockIdx.x, st = 0, issued = 0, queries[2] = {0, 0};
+            bool asked = false;
             uint32_t parity = 1;                 // of the slot's previous release (none in the first round)
-            for (int i = 0; i < 2 * n; ++i) {
-                if (queries < 2 && (queries == 0 || n1 > 0)) {
-                    load(base + queries * C::kTileBytes, &qmap, head0 + queries * head_step,
-                         row0 + q0 + queries * tok_step, &bars[C::kQFull + queries]);
-                    ++queries;
-                }
-                if (i >= C::kStages && !(ok = mbar_wait_or_abort(&bars[C::kFree + st], parity, abort_flag)))
+            for (int d = 0;; ++d) {
+                if (d >= 2 && !(ok = mbar_wait_or_abort(&bars[C::kWorkFree + (d & 1)], (d / 2 - 1) & 1u, abort_flag)))
                     break;
-                load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head,
-                     row0 + (i >> 1) * kTile, &bars[C::kFull + st]);
-                issued = i + 1;
-                if (++st == C::kStages) {
-                    st = 0;
-                    parity ^= 1u;
+                Work w{0, -1, 0, 0};
+                if (block >= 0) {
+                    const int item = block / units;
+                    const int32_t *it = p.items + (int64_t)item * kItemFields;
+                    w = Work{it[0], it[1], it[2], block - item * units};
+                    if (w.row0 < 0 || w.len < 1 || w.len > p.num_rows - w.row0 || w.q0 < 0 || w.q0 >= w.len ||
+                        w.q0 % kTile != 0) {
+                        record_error(p.err, RLT_DEVERR_BAD_LEN);   // a plan of other sequences
+                        w.len = w.q0 = 0;
+                    }
                 }
+                works[d & 1].row0 = w.row0;
+                works[d & 1].len = w.len;
+                works[d & 1].q0 = w.q0;
+                works[d & 1].unit = w.unit;
+                mbar_arrive(&bars[C::kWorkFull + (d & 1)]);
+                if (w.len < 0)
+                    break;
+                mbar_arrive_expect_tx(&bars[C::kNext], 16);
+                ask_for_block(base + C::kNextOff, &bars[C::kNext]);
+                asked = true;
+                const int head0 = pair ? 2 * w.unit : w.unit, kv_head = head0 / G;
+                const int n = max(key_tiles(w, 0), key_tiles(w, 1));
+                for (int i = 0; ok && i < 2 * n; ++i) {
+                    if (i < 2) {
+                        if (d > 0 && !(ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag)))
+                            break;
+                        if (key_tiles(w, i) > 0) {
+                            load(base + i * C::kTileBytes, &qmap, head0 + i * head_step, w.row0 + w.q0 + i * tok_step,
+                                 &bars[C::kQFull + i]);
+                            queries[i] = 1;
+                        } else {
+                            mbar_arrive(&bars[C::kQFull + i]);
+                        }
+                    }
+                    if (issued >= C::kStages && !(ok = mbar_wait_or_abort(&bars[C::kFree + st], parity, abort_flag)))
+                        break;
+                    load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head,
+                         w.row0 + (i >> 1) * kTile, &bars[C::kFull + st]);
+                    ++issued;
+                    if (++st == C::kStages) {
+                        st = 0;
+                        parity ^= 1u;
+                    }
+                }
+                if (n == 0) {                    // (keeps the Q barriers' phases one a work)
+                    for (int i = 0; ok && i < 2; ++i) {
+                        if (d > 0)
+                            ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag);
+                        mbar_arrive(&bars[C::kQFull + i]);
+                    }
+                }
+                if (!ok || !(ok = mbar_wait_or_abort(&bars[C::kNext], d & 1u, abort_flag)))
+                    break;
+                asked = false;
+                block = answered_block(base + C::kNextOff);
+                fence_proxy_async();             // the answer has been read before the next one is written
             }
-            if (!ok)
+            if (!ok) {
                 *abort_flag = 1;
-            // every copy has landed before the CTA gives up its memory (bounded; on the normal path
-            // the products have waited for all of them)
-            for (int i = max(0, issued - C::kStages); i < issued; ++i)
-                mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
-            for (int i = 0; i < queries; ++i)
-                mbar_wait(&bars[C::kQFull + i], 0);
+                // every copy and the scheduler's answer have landed before the CTA gives up its memory (bounded;
+                // on the normal path the other roles have waited for all of them)
+                for (int i = max(0, issued - C::kStages); i < issued; ++i)
+                    mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
+                for (uint64_t t0 = global_ns(); (asked || queries[0] || queries[1]) && global_ns() - t0 < kWaitLimitNs / 100;)
+                    ;
+            }
         } else if (warp < kLoadWarp && tc::elect_one()) {
             // ---------------------------------------------------------- products
             // One thread a tile, in the order S | PV S' | PV' S'' ...: MMAs of one thread run in issue order,
             // so S of the next key tile may overwrite the P that the PV before it reads.  A wait costs a thread
-            // about 75 clocks and a full MMA queue holds it up; with a thread a tile neither delays the
-            // other tile's products (one thread for both measured 352 us where two take 322: 8192
-            // tokens, 32 heads).  An MMA keeps the tensor pipe 64 clocks, so its issue has to take
-            // less: the descriptors are the tile's plus constants.
+            // about 75 clocks and a full MMA queue holds it up; with a thread a tile neither delays the other
+            // tile's products.  An MMA keeps the tensor pipe 64 clocks, so its issue has to take less: the
+            // descriptors are the tile's plus constants.
             const int s = warp - kMmaWarp;
-            const int ns = s == 0 ? n0 : n1;
             constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
             constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
-            constexpr uint64_t kTileStep = C::kTileBytes >> 4;
-            const uint64_t qd = tc::smem_desc(smem_u32(base), 16, 1024) + s * kTileStep;
-            const uint64_t kd = tc::smem_desc(smem_u32(base + C::kRingOff), 16, 1024);
-            const uint64_t vd = tc::smem_desc(smem_u32(base + C::kRingOff), C::kBlock, 1024);
+            // Descriptors: the low words (address and leading offset, both in 16 bytes) advance, the high word
+            // (stride 1024, 128-byte swizzle) is tc::smem_desc's constant.
+            constexpr uint32_t kTileStep = C::kTileBytes >> 4, kBlockStep = C::kBlock >> 4;
+            const uint32_t qd = (uint32_t)tc::smem_desc(smem_u32(base), 16, 1024) + s * kTileStep;
+            const uint32_t kd = (uint32_t)tc::smem_desc(smem_u32(base + C::kRingOff), 16, 1024);
+            const uint32_t vd = (uint32_t)tc::smem_desc(smem_u32(base + C::kRingOff), C::kBlock, 1024);
+            auto desc = [&](uint32_t low) -> uint64_t {
+                constexpr uint32_t kHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+                return ((uint64_t)kHigh << 32) | low;
+            };
             const uint32_t t_s = tmem + kColS + s * kTile, t_o = tmem + kColO + s * kTile;
             auto issue_s = [&](int slot) {
-                const uint64_t b = kd + slot * kTileStep;
+                const uint32_t b = kd + slot * kTileStep;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    constexpr uint64_t kStep = C::kBlock >> 4;
-                    tc::mma_bf16(t_s, qd + (kk >> 2) * kStep + (kk & 3) * 2, b + (kk >> 2) * kStep + (kk & 3) * 2, id_s,
-                                 kk > 0);
+                    const uint32_t at = (kk >> 2) * kBlockStep + (kk & 3) * 2;
+                    tc::mma_bf16(t_s, desc(qd + at), desc(b + at), id_s, kk > 0);
                 }
                 tc::mma_commit(&bars[C::kSFull + s]);
             };
             auto issue_pv = [&](int half, int slot, bool first) {             // 64 keys
-                const uint64_t b = vd + slot * kTileStep + half * (4 * 2048 >> 4);
+                const uint32_t b = vd + slot * kTileStep + half * (4 * 2048 >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_bf16_ta(t_o, t_s + half * 32 + kk * 8, b + kk * (2048 >> 4), id_o, kk > 0 || !first);
+                    tc::mma_bf16_ta(t_o, t_s + half * 32 + kk * 8, desc(b + kk * (2048 >> 4)), id_o, kk > 0 || !first);
             };
             // ring slot and parity of the next copy to be waited for
             int st = 0;
@@ -222,64 +328,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             // a tile without work on a copy lets it go at once
-            auto release = [&](int slot, bool used) {
+            auto release = [&](int bar, bool used) {
                 if (used)
-                    tc::mma_commit(&bars[C::kFree + slot]);
+                    tc::mma_commit(&bars[bar]);
                 else
-                    mbar_arrive(&bars[C::kFree + slot]);
+                    mbar_arrive(&bars[bar]);
             };
-            int k_slot = 0, v_slot = 0, s_issued = 0, pv_issued = 0;
-            ok = wait_slot(k_slot) && (ns == 0 || mbar_wait_or_abort(&bars[C::kQFull + s], 0, abort_flag));
-            if (ok) {
-                if (ns > 0) {
-                    issue_s(k_slot);
-                    s_issued = 1;
-                }
-                release(k_slot, ns > 0);
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                if (!(ok = wait_slot(v_slot)) || (j + 1 < n && !(ok = wait_slot(k_slot))))
+            int tiles = 0, items = 0, s_issued = 0;   // key tiles and works with rows, over all works
+            for (int d = 0;; ++d) {
+                if (!(ok = mbar_wait_or_abort(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag)))
                     break;
-                if (j < ns) {
-                    if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], j & 1u, abort_flag)))
+                Work w;
+                take(d, w);
+                if (w.len < 0)
+                    break;
+                const int ns = key_tiles(w, s), n = max(key_tiles(w, 0), key_tiles(w, 1));
+                int k_slot = 0, v_slot = 0;
+                if (!(ok = mbar_wait_or_abort(&bars[C::kQFull + s], d & 1u, abort_flag)))
+                    break;
+                if (n > 0) {
+                    if (!(ok = wait_slot(k_slot)))
                         break;
-                    tc::fence_after_sync();
-                    issue_pv(0, v_slot, j == 0);
-                    pv_issued = j + 1;
-                    ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], j & 1u, abort_flag);
-                    tc::fence_after_sync();
-                    if (ok)
-                        issue_pv(1, v_slot, false);
-                    tc::mma_commit(&bars[C::kPvDone + s]);
-                    if (!ok)
-                        break;
-                    if (j + 1 < ns) {
+                    if (ns > 0) {
                         issue_s(k_slot);
-                        s_issued = j + 2;
+                        ++s_issued;
                     }
+                    release(C::kFree + k_slot, ns > 0);
                 }
-                release(v_slot, j < ns);
-                if (j + 1 < n)
-                    release(k_slot, j + 1 < ns);
+                if (ns <= 1)
+                    release(C::kQFree + s, ns > 0);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (!(ok = wait_slot(v_slot)) || (j + 1 < n && !(ok = wait_slot(k_slot))))
+                        break;
+                    if (j < ns) {
+                        // the item before has left O
+                        if (j == 0 && items > 0 &&
+                            !(ok = mbar_wait_or_abort(&bars[C::kOFree + s], (items - 1) & 1u, abort_flag)))
+                            break;
+                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], tiles & 1u, abort_flag)))
+                            break;
+                        tc::fence_after_sync();
+                        issue_pv(0, v_slot, j == 0);
+                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], tiles & 1u, abort_flag)))
+                            break;
+                        tc::fence_after_sync();
+                        issue_pv(1, v_slot, false);
+                        ++tiles;
+                        if (j + 1 < ns) {
+                            issue_s(k_slot);
+                            ++s_issued;
+                            if (j + 2 == ns)
+                                tc::mma_commit(&bars[C::kQFree + s]);
+                        } else {
+                            tc::mma_commit(&bars[C::kODone + s]);
+                            ++items;
+                        }
+                    }
+                    release(C::kFree + v_slot, j < ns);
+                    if (j + 1 < n)
+                        release(C::kFree + k_slot, j + 1 < ns);
+                }
+                if (!ok)
+                    break;
+                mbar_arrive(&bars[C::kWorkFree + (d & 1)]);
             }
             if (!ok)
                 *abort_flag = 1;
-            // every issued MMA is complete before the CTA gives up its memory (bounded)
-            if (pv_issued > 0)
-                mbar_wait(&bars[C::kPvDone + s], (pv_issued - 1) & 1u);
-            if (s_issued > pv_issued)
-                mbar_wait(&bars[C::kSFull + s], (s_issued - 1) & 1u);
+            // every issued MMA is complete before the CTA gives up its memory (bounded).  On the normal path the
+            // last ODone covers all; after an abort, the last S and some time for a P V half behind it
+            if (ok) {
+                if (items > 0)
+                    mbar_wait(&bars[C::kODone + s], (items - 1) & 1u);
+            } else {
+                if (s_issued > 0)
+                    mbar_wait(&bars[C::kSFull + s], (s_issued - 1) & 1u);
+                for (uint64_t t0 = global_ns(); global_ns() - t0 < kWaitLimitNs / 100;)
+                    ;
+            }
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ---------------------------------------------------------- softmax
         const int s = warp >> 2, quarter = warp & 3;
-        const int ns = s == 0 ? n0 : n1;
-        const int q_tok = q0 + s * tok_step + quarter * 32 + lane;       // this thread's query, in its sequence
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t t_s = t_lane + kColS + s * kTile, t_o = t_lane + kColO + s * kTile;
-        float m_ref = -CUDART_INF_F, l_run = 0.f;
         auto p_ready = [&](int half) {           // this warp's P of 64 keys is in tensor memory
             tc::tmem_wait_st();
             tc::fence_before_sync();
@@ -287,129 +420,202 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(&bars[C::kPFull + 2 * s + half]);
         };
-        for (int j = 0; j < ns; ++j) {
-            if (!(ok = warp_wait(&bars[C::kSFull + s], j & 1u, abort_flag)))
+        int tiles = 0, items = 0, copies = 0;    // of this tile, and of the ring before this work
+        for (int d = 0;; ++d) {
+            if (!(ok = warp_wait(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag)))
                 break;
-            tc::fence_after_sync();
-            if (j == ns - 1 && (j + 1) * kTile > len && quarter == 0) {
-                // ragged end of the sequence: the V rows past it may hold anything (0 * NaN would
-                // poison O): zeros, once the copy has landed
-                const int i = 2 * j + 1;
-                if (!(ok = warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag)))
-                    break;
-                unsigned char *vt = base + C::kRingOff + i % C::kStages * C::kTileBytes;
-                const int valid = len - j * kTile;
-                for (int c = lane; c < (kTile - valid) * kBlocks * 8; c += 32) {
-                    const int r = valid + c / (kBlocks * 8), c16 = c % (kBlocks * 8);
-                    *reinterpret_cast<uint4 *>(vt + (c16 >> 3) * C::kBlock + r * 128 + (c16 & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async();
-            }
-            float v[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tc::tmem_ld32_nowait(t_s + c * 32, v[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tc::tmem_wait_ld(v[c]);
-            if (j == ns - 1) {                   // the diagonal: keys behind the query
-                const int last = q_tok - j * kTile;
-#pragma unroll
-                for (int i = 0; i < kTile; ++i)
-                    v[i / 32][i % 32] = i <= last ? v[i / 32][i % 32] : -CUDART_INF_F;
-            }
-            // P = 2^(s - m), 32 columns at a time.  The first ones are made against the reference the row has,
-            // beside the row's maximum: it moves rarely, and then they are made again.  The exponentials
-            // of the next columns are issued ahead of the conversions of the last ones: the unit
-            // that makes them (8 lanes a clock) is what a warp waits for.
-            auto raise = [&](const float (&x)[32], float (&y)[32], float m) {
-                const float m_sub = m == -CUDART_INF_F ? 0.f : m;
-                const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 z = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
-                    y[2 * i] = exp2_in_order(z.x);
-                    y[2 * i + 1] = exp2_in_order(z.y);
-                }
-            };
-            uint64_t sum2[2] = {0ull, 0ull};
-            auto store = [&](const float (&y)[32], int c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = cvt_bf16x2(y[2 * i], y[2 * i + 1]);
-                tc::tmem_st_nowait<16>(t_s + c * 16, w);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(y[2 * i], y[2 * i + 1]));
-            };
-            float y0[32];
-            raise(v[0], y0, m_ref);
-            float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx4[k] = fmaxf(fmaxf(mx4[k], v[c][i + k]), v[c][i + 4 + k]);
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
-            const bool up = mx > m_ref + kRescaleThreshold;
-            if (__any_sync(kFullMask, up)) {
-                const float m_next = up ? mx : m_ref;
-                const float scale_o = m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
-                if (j > 0) {
-                    if (!(ok = warp_wait(&bars[C::kPvDone + s], (j - 1) & 1u, abort_flag)))
+            Work wk;
+            take(d, wk);
+            if (wk.len < 0)
+                break;
+            const int ns = key_tiles(wk, s), n = max(key_tiles(wk, 0), key_tiles(wk, 1));
+            const int q_tok = wk.q0 + s * tok_step + quarter * 32 + lane;    // this thread's query, in its sequence
+            const int head0 = pair ? 2 * wk.unit : wk.unit;
+            uint32_t *bad = reinterpret_cast<uint32_t *>(base + C::kBadOff) + (d & 1) * 8;
+            if (ns == 0 && lane == 0)
+                bad[s * 4 + quarter] = 0u;
+            float m_ref = -CUDART_INF_F, l_run = 0.f;
+            for (int j = 0; j < ns; ++j, ++tiles) {
+                if (j == ns - 1) {
+                    // The tile of the row's own keys: weights of masked keys are 0, but 0 times an infinity or NaN
+                    // would stay.  Rows of V past the sequence (they may hold anything) become zeros, and so do
+                    // single values that are not finite; their rows are noted, and the epilogue adds what
+                    // a query may see of them.  A lane looks at one row, while S is computed.
+                    const int i = copies + 2 * j + 1;
+                    if (!(ok = warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag)))
                         break;
-                    tc::fence_after_sync();
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        float o[16];
-                        uint32_t ow[16];
-                        tc::tmem_ld<16>(t_o + c * 16, o);
+                    unsigned char *vt = base + C::kRingOff + i % C::kStages * C::kTileBytes;
+                    const int r = quarter * 32 + lane;
+                    const bool inside = r < wk.len - j * kTile;
+                    uint32_t big = 0u;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            ow[i] = __float_as_uint(o[i] * scale_o);
-                        tc::tmem_st_nowait<16>(t_o + c * 16, ow);
+                    for (int c = 0; c < kBlocks * 8; ++c) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::kBlock + r * 128 +
+                                                                         (((c ^ r) & 7) << 4));
+                        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                    }
+                    const unsigned odd = __ballot_sync(kFullMask, inside && not_finite(big));
+                    if (lane == 0)
+                        bad[s * 4 + quarter] = odd;
+                    __threadfence_block();       // the note before the values go
+                    __syncwarp();
+                    if (!inside || not_finite(big)) {
+#pragma unroll 1
+                        for (int c = 0; c < kBlocks * 8; ++c) {
+                            uint4 *at = reinterpret_cast<uint4 *>(vt + (c >> 3) * C::kBlock + r * 128 +
+                                                                  (((c ^ r) & 7) << 4));
+                            uint4 x = *at;
+                            auto clean = [&](uint32_t y) -> uint32_t {
+                                if (!inside)
+                                    return 0u;
+                                return ((y & 0x7f80u) == 0x7f80u ? 0u : y & 0xffffu) |
+                                       ((y & 0x7f800000u) == 0x7f800000u ? 0u : y & 0xffff0000u);
+                            };
+                            *at = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+                        }
+                        fence_proxy_async();     // (generic writes before the product's reads)
+                    }
+                    __syncwarp();
+                }
+                if (!(ok = warp_wait(&bars[C::kSFull + s], tiles & 1u, abort_flag)))
+                    break;
+                tc::fence_after_sync();
+                float v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tc::tmem_ld32_nowait(t_s + c * 32, v[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tc::tmem_wait_ld(v[c]);
+                if (j == ns - 1) {                   // the diagonal: keys behind the query
+                    const int last = q_tok - j * kTile;
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i)
+                        v[i / 32][i % 32] = i <= last ? v[i / 32][i % 32] : -CUDART_INF_F;
+                }
+                // P = 2^(s - m), 32 columns at a time.  The first ones are made against the reference the row has,
+                // beside the row's maximum: it moves rarely, and then they are made again.  The exponentials
+                // of the next columns are issued ahead of the conversions of the last ones: the unit
+                // that makes them (8 lanes a clock) is what a warp waits for.
+                auto raise = [&](const float (&x)[32], float (&y)[32], float m) {
+                    const float m_sub = m == -CUDART_INF_F ? 0.f : m;
+                    const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 z = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
+                        y[2 * i] = exp2_in_order(z.x);
+                        y[2 * i + 1] = exp2_in_order(z.y);
+                    }
+                };
+                uint64_t sum2[2] = {0ull, 0ull};
+                auto store = [&](const float (&y)[32], int c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = cvt_bf16x2(y[2 * i], y[2 * i + 1]);
+                    tc::tmem_st_nowait<16>(t_s + c * 16, w);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(y[2 * i], y[2 * i + 1]));
+                };
+                float y0[32];
+                raise(v[0], y0, m_ref);
+                float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx4[k] = fmaxf(fmaxf(mx4[k], v[c][i + k]), v[c][i + 4 + k]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
+                const bool up = mx > m_ref + kRescaleThreshold;
+                if (__any_sync(kFullMask, up)) {
+                    const float m_next = up ? mx : m_ref;
+                    const float scale_o = m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
+                    if (j > 0) {                     // (S of this tile is behind the products of the last)
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            uint32_t ow[16];
+                            tc::tmem_ld<16>(t_o + c * 16, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                ow[i] = __float_as_uint(o[i] * scale_o);
+                            tc::tmem_st_nowait<16>(t_o + c * 16, ow);
+                        }
+                    }
+                    l_run *= scale_o;
+                    m_ref = m_next;
+                    raise(v[0], y0, m_ref);
+                }
+                raise(v[1], v[1], m_ref);
+                store(y0, 0);
+                raise(v[2], v[2], m_ref);
+                store(v[1], 1);
+                p_ready(0);                          // the first 64 keys' weights
+                raise(v[3], v[3], m_ref);
+                store(v[2], 2);
+                store(v[3], 3);
+                p_ready(1);
+                const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
+                l_run += sum.x + sum.y;
+            }
+            if (ok && ns > 0 && (ok = warp_wait(&bars[C::kODone + s], items & 1u, abort_flag))) {
+                tc::fence_after_sync();
+                ++items;
+                const float inv = 1.f / l_run;
+                const int64_t at = (int64_t)(wk.row0 + q_tok) * p.num_q_heads + head0 + s * head_step;
+                // rows of V with values that are not finite: of both tiles' last keys (cleaned by either)
+                uint32_t any_bad = 0u;
+                for (int i = 0; i < 8; ++i)
+                    any_bad |= reinterpret_cast<volatile uint32_t *>(bad)[i];
+                float o[D / 32][32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    tc::tmem_ld32_nowait(t_o + c * 32, o[c]);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    tc::tmem_wait_ld(o[c]);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars[C::kOFree + s]);
+                if (any_bad != 0u) {
+#pragma unroll 1
+                    for (int b = 0; b < 256; ++b) {
+                        const int key = wk.q0 + (b >> 7) * tok_step + (b & 127);
+                        if (((reinterpret_cast<volatile uint32_t *>(bad)[b >> 5] >> (b & 31)) & 1u) == 0u ||
+                            key > q_tok || key >= wk.len)
+                            continue;
+                        const uint16_t *vr = p.v + (int64_t)(wk.row0 + key) * p.v_stride + (int64_t)(head0 / G) * D;
+#pragma unroll
+                        for (int c = 0; c < D; ++c) {
+                            const uint32_t x = vr[c];
+                            if ((x & 0x7f80u) == 0x7f80u)
+                                o[c / 32][c % 32] += __uint_as_float(x << 16);
+                        }
                     }
                 }
-                l_run *= scale_o;
-                m_ref = m_next;
-                raise(v[0], y0, m_ref);
-            }
-            raise(v[1], v[1], m_ref);
-            store(y0, 0);
-            raise(v[2], v[2], m_ref);
-            store(v[1], 1);
-            p_ready(0);                          // the first 64 keys' weights
-            raise(v[3], v[3], m_ref);
-            store(v[2], 2);
-            store(v[3], 3);
-            p_ready(1);
-            const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
-            l_run += sum.x + sum.y;
-        }
-        if (ok && ns > 0 && (ok = warp_wait(&bars[C::kPvDone + s], (ns - 1) & 1u, abort_flag))) {
-            tc::fence_after_sync();
-            const float inv = 1.f / l_run;
-            const int64_t at = (int64_t)(row0 + q_tok) * p.num_q_heads + head0 + s * head_step;
+                if (q_tok < wk.len) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tc::tmem_ld<32>(t_o + c * 32, o);
-                if (q_tok < len) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + c * 32);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(cvt_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                            cvt_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                            cvt_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                            cvt_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    for (int i = 0; i < D / 8; ++i) {
+                        const float *x = &o[i / 4][i % 4 * 8];
+                        dst[i] = make_uint4(cvt_bf16x2(x[0] * inv, x[1] * inv), cvt_bf16x2(x[2] * inv, x[3] * inv),
+                                            cvt_bf16x2(x[4] * inv, x[5] * inv), cvt_bf16x2(x[6] * inv, x[7] * inv));
+                    }
+                    if (p.lse_out != nullptr)
+                        p.lse_out[at] = (m_ref + log2f(l_run)) * 0.6931471805599453f;
                 }
             }
-            if (q_tok < len && p.lse_out != nullptr)
-                p.lse_out[at] = (m_ref + log2f(l_run)) * 0.6931471805599453f;
+            if (!ok)
+                break;
+            copies += 2 * n;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&bars[C::kWorkFree + (d & 1)]);
         }
         if (!ok)
             *abort_flag = 1;

@@ -108,6 +108,61 @@ def test_neighbours_and_rows_behind_hold_anything(dev):
     assert (out[320:] == 9).all() and (lse[320:] == 9).all()
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (3, 3, 64), (3, 1, 128), (8, 2, 64)])
+def test_values_a_query_may_not_see(dev, hq, hkv, d):
+    """Infinities and NaN in V reach exactly the queries at or behind them (as the formula has it: a NaN every one of
+    them, an infinity unless it meets its opposite); NaN in K of later keys reaches nobody before."""
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    lens = [300, 90, 260]
+    n = sum(lens)
+    q, k, v = rows(torch, dev, n, hq, hkv, d, 11, fused=False)
+    plan = rlt.rlt_plan_prefill(lens, hq // hkv)
+    lse, clean_lse = torch.empty(n, hq, device=dev), torch.empty(n, hq, device=dev)
+    clean = rlt.rlt_prefill_attn(q, k, v, plan, lse_out=clean_lse)
+    odd = [(70, 3, float("nan")), (200, d - 1, float("inf")), (200, 5, float("-inf")), (299, 0, float("nan")),
+           (300, 7, float("inf")), (389, 7, float("-inf")), (640, 9, float("nan"))]
+    want = clean.clone()
+    first = [0, 300, 390]
+    for row, c, x in odd:
+        v[row, 0, c] = x
+        seq = max(i for i in range(3) if first[i] <= row)
+        want[row:first[seq] + lens[seq], :hq // hkv, c] = float("nan") if x != x or (row, c) == (389, 7) else x
+    out = rlt.rlt_prefill_attn(q, k, v, plan, lse_out=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    same = ~torch.isnan(want)
+    assert torch.equal(torch.isinf(out[same]), torch.isinf(want[same])) and torch.equal(out[same].sign(), want[same].sign())
+    fin = torch.isfinite(want)
+    assert torch.equal(out[fin], clean[fin]) and torch.equal(lse, clean_lse)
+    v.copy_(torch.where(torch.isfinite(v), v, 0.0))
+    base = rlt.rlt_prefill_attn(q, k, v, plan)
+    k[250] = float("nan")
+    out = rlt.rlt_prefill_attn(q, k, v, plan, lse_out=lse)
+    torch.cuda.synchronize()
+    keep = list(range(250)) + list(range(300, n))
+    assert torch.equal(out[keep], base[keep]) and torch.isnan(out[250:300]).all() and torch.isnan(lse[250:300]).all()
+    assert rlt.rlt_get_device_error() == 0
+
+
+def test_many_items(dev):
+    """More work than the GPU holds at once, of every size: blocks hand their work over to running ones."""
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 400, (300,), generator=g).tolist()
+    for hq, hkv, d in ((8, 2, 128), (3, 1, 64)):
+        n = sum(lens)
+        q, k, v = rows(torch, dev, n, hq, hkv, d, 12)
+        plan = rlt.rlt_plan_prefill(lens, hq // hkv).to(dev)
+        lse = torch.empty(n, hq, device=dev)
+        out = [rlt.rlt_prefill_attn(q, k, v, plan, lse_out=lse) for _ in range(5)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, out[0]) for o in out[1:])
+        assert rlt.rlt_get_device_error() == 0
+        check(out[0], lse, q, k, v, lens, 1 / np.sqrt(d))
+
+
 def test_streams_and_graph(dev):
     import torch
     import paged_kv_looped_gb300 as rlt
