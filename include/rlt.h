@@ -601,8 +601,10 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
  *              are neither looked at nor written
  *   items      the plan, DEVICE copy; an item outside num_rows is skipped and sets
  *              RLT_DEVERR_BAD_LEN
+ *   max_key_tiles, total_key_tiles  sizes[2] and sizes[3] of the plan: how heads are grouped for
+ *              L2 (any value gives the same result)
  *   scale      softmax scale; <= 0 means 1/sqrt(head_dim)
- *   out        bf16 [num_rows][num_q_heads][head_dim], 16-byte aligned, apart from q, k, v
+ *   out        bf16 [num_rows][num_q_heads][head_dim], 32-byte aligned, apart from q, k, v
  *   lse_out    fp32 [num_rows][num_q_heads], natural log, or NULL
  *   flags      0 or RLT_ATTN_EARLY_START (no kernel still running ahead may write items)
  * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
@@ -614,7 +616,7 @@ RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t batch, int3
 RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t q_stride, const void *k,
                                     int64_t k_stride, const void *v, int64_t v_stride, int32_t num_kv_heads,
                                     int32_t head_dim, int32_t num_rows, const int32_t *items, int32_t num_items,
-                                    float scale, void *out, float *lse_out, uint32_t flags, void *stream);
+                                    int32_t max_key_tiles, int32_t total_key_tiles, float scale, void *out, float *lse_out, uint32_t flags, void *stream);
 
 /*
  * HOST validation of a decode batch before it is handed to the GPU (all

@@ -119,7 +119,7 @@ def load():
         "rlt_paged_decode_attn_kv8": (ctypes.c_int, [pool8_p, i32, P, i32, P, i32, P, i32, i32, f32, P, P, P, sz, i32,
                                                      u32, P]),
         "rlt_plan_prefill": (ctypes.c_int, [P, i32, i32, P, i32, P]),
-        "rlt_prefill_attn": (ctypes.c_int, [P, i32, i64, P, i64, P, i64, i32, i32, i32, P, i32, f32, P, P, u32, P]),
+        "rlt_prefill_attn": (ctypes.c_int, [P, i32, i64, P, i64, P, i64, i32, i32, i32, P, i32, i32, i32, f32, P, P, u32, P]),
         "rlt_plan_extend": (ctypes.c_int, [P, P, i32, i32, i32, i32, P, i32, P, P, i32, P, P, P]),
         "rlt_paged_extend_workspace_size": (sz, [i32, i32, i32, i32]),
         "rlt_paged_extend_attn": (ctypes.c_int, [pool_p, i32, P, i32, i32, P, i32, i32, P, P, P, P, P, i32, i32,
@@ -757,8 +757,9 @@ def rlt_paged_decode_attn_kv8(pool: KV8Pool, bank: int, q, page_table, seq_lens,
 class PrefillPlan:
     """Host output of rlt_plan_prefill; .to(device) uploads it for rlt_prefill_attn."""
 
-    def __init__(self, items, num_rows, query_group):
-        self.items, self.num_items, self.num_rows, self.query_group = items, len(items), num_rows, query_group
+    def __init__(self, items, sizes, query_group):
+        self.items, self.query_group = items, query_group
+        self.num_items, self.num_rows, self.max_key_tiles, self.total_key_tiles = (int(x) for x in sizes)
         self.dev = None
 
     def to(self, device):
@@ -771,14 +772,14 @@ def rlt_plan_prefill(seq_lens, query_group: int = 1) -> PrefillPlan:
     """Work items of causal attention over sequences of these lengths, packed one after another.
     ``query_group`` = num_q_heads / num_kv_heads of the attention the plan is for."""
     sl, slp = _host(seq_lens, np.int32)
-    sizes = np.zeros(2, np.int32)
+    sizes = np.zeros(4, np.int32)
     st = load().rlt_plan_prefill(slp, sl.size, int(query_group), ctypes.c_void_p(0), 0, _np_ptr(sizes))
     if st not in (0, 2):
         _check(st, "rlt_plan_prefill")
     items = np.zeros((int(sizes[0]), 4), np.int32)
     _check(load().rlt_plan_prefill(slp, sl.size, int(query_group), _np_ptr(items), items.shape[0], _np_ptr(sizes)),
            "rlt_plan_prefill")
-    return PrefillPlan(items, int(sizes[1]), int(query_group))
+    return PrefillPlan(items, sizes, int(query_group))
 
 
 def _np_ptr(a):
@@ -809,7 +810,8 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
         _record(stream, out)
     _same_device(q, k, v, plan.dev, out, lse_out)
     _check(load().rlt_prefill_attn(
-        qp, Hq, qs, kp, ks, vp, vs, Hkv, D, N, _ptr(plan.dev, torch.int32, "plan"), plan.num_items, float(scale),
+        qp, Hq, qs, kp, ks, vp, vs, Hkv, D, N, _ptr(plan.dev, torch.int32, "plan"), plan.num_items,
+        plan.max_key_tiles, plan.total_key_tiles, float(scale),
         _ptr(out, torch.bfloat16, "out", (N, Hq, D)), _ptr(lse_out, torch.float32, "lse_out", (N, Hq)),
         ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_prefill_attn")
     return out

@@ -208,9 +208,10 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
 RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t q_stride, const void *k,
                                     int64_t k_stride, const void *v, int64_t v_stride, int32_t num_kv_heads,
                                     int32_t head_dim, int32_t num_rows, const int32_t *items, int32_t num_items,
-                                    float scale, void *out, float *lse_out, uint32_t flags, void *stream)
+                                    int32_t max_key_tiles, int32_t total_key_tiles, float scale, void *out, float *lse_out, uint32_t flags, void *stream)
 {
-    if ((flags & ~RLT_ATTN_EARLY_START) != 0 || num_rows < 0 || num_items < 0 || num_kv_heads < 1 || num_q_heads < 1 ||
+    if ((flags & ~RLT_ATTN_EARLY_START) != 0 || num_rows < 0 || num_items < 0 || max_key_tiles < 0 ||
+        total_key_tiles < 0 || num_kv_heads < 1 || num_q_heads < 1 ||
         num_q_heads % num_kv_heads != 0 || !std::isfinite(scale))
         return RLT_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || (int64_t)num_items * num_q_heads > INT32_MAX)
@@ -219,7 +220,7 @@ RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t 
         return RLT_OK;
     const int64_t q_width = (int64_t)num_q_heads * head_dim, kv_width = (int64_t)num_kv_heads * head_dim;
     if (num_rows < 1 || q == nullptr || k == nullptr || v == nullptr || items == nullptr || out == nullptr ||
-        !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+        !aligned16(q) || !aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(out) % 32 != 0 ||
         reinterpret_cast<uintptr_t>(items) % 4 != 0 || reinterpret_cast<uintptr_t>(lse_out) % 4 != 0)
         return RLT_ERR_INVALID_ARG;
     if (q_stride < q_width || k_stride < kv_width || v_stride < kv_width || q_stride % 8 != 0 || k_stride % 8 != 0 ||
@@ -230,9 +231,13 @@ RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t 
         clashes(to, {v, num_rows, kv_width, v_stride}, false))
         return RLT_ERR_INVALID_ARG;
     rlt::PrefillParams p{};
-    rlt_status st = rlt::current_device_info(&p.err, nullptr);
+    int sms = 0;
+    rlt_status st = rlt::current_device_info(&p.err, &sms);
     if (st != RLT_OK)
         return st;
+    p.max_tiles = max_key_tiles;
+    p.total_tiles = total_key_tiles;
+    p.num_sms = sms;
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k);
     p.v = static_cast<const uint16_t *>(v);

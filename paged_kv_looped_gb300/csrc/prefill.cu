@@ -42,15 +42,19 @@ constexpr int kThreads = 12 * 32;            // warp 11 only fills the third war
 constexpr int kRegsSoftmax = 208, kRegsRest = 88;
 constexpr float kRescaleThreshold = 8.f;     // log2 units
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
+constexpr int kPartsFrom = 6;                // items of the largest size an SM's share has to hold
+constexpr int64_t kL2Share = 48 << 20;       // of K and V in use at a time (L2 is 126 MB)
+constexpr int kOutBytes = 32 * 128;
 constexpr int kItemFields = 4;               // first row of the sequence, its length, first query of the item, 0
 
 template <int D>
 struct PCfg {
-    static constexpr int kStages = D == 128 ? 5 : 8;             // K/V ring slots
+    static constexpr int kStages = D == 128 ? 4 : 8;             // K/V ring slots
     static constexpr int kBlock = kTile * 128;                   // a 64-dim column block of a tile
     static constexpr int kTileBytes = D / 64 * kBlock;
     static constexpr int kRingOff = 2 * kTileBytes;              // behind the two Q tiles
-    static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+    static constexpr int kOutOff = kRingOff + kStages * kTileBytes;   // 32 rows x 64 dims of output a softmax warp
+    static constexpr int kBarOff = kOutOff + 8 * kOutBytes;
     enum Bar {
         kQFull = 0,                          // [tile] the item's Q landed
         kQFree = kQFull + 2,                 // [tile] read by its last S
@@ -70,6 +74,7 @@ struct PCfg {
     static constexpr int kBadOff = kNextOff + 16;                // [2 items][tile][4] rows with non-finite values
     static constexpr int kFlagOff = kBadOff + 64;
     static constexpr int kSmem = kFlagOff + 16 + 1024;
+    static_assert(kNumBars <= kThreads, "a thread a barrier at the start");
 };
 
 // One work item: query rows q0.. of a sequence (rows row0 .. row0 + len - 1) for one unit of heads.
@@ -85,6 +90,15 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+
+// The box at (x, y, z) from shared memory, as a bulk group of the calling thread.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int32_t x, int32_t y, int32_t z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
 }
 
 // Cluster launch control: asks the hardware scheduler for the block of this grid it would start next.  The
@@ -127,13 +141,22 @@ __device__ __forceinline__ float exp2_in_order(float x)
     return r;
 }
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store_sector(void *dst, const uint32_t (&y)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                 "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                 : "memory");
+}
+
 // Whether a word of two bf16 values holds an infinity or NaN, from the larger magnitude's bits.
 __device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0xffffu) >= 0x7f80u || bits >= 0x7f800000u; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const PrefillParams p)
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
+                   const PrefillParams p)
 {
     using C = PCfg<D>;
     constexpr int kBlocks = D / 64;
@@ -152,18 +175,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int units = pair ? p.num_q_heads / 2 : p.num_q_heads;
     const int head_step = pair ? 1 : 0, tok_step = pair ? 0 : kTile;
 
-    if (tid == 0) {
-        for (int i = 0; i < C::kNumBars; ++i) {
-            int count = 1;
-            if (i >= C::kFree && i < C::kSFull)
-                count = 2;                       // both tiles' MMA threads
-            else if ((i >= C::kPFull && i < C::kODone) || (i >= C::kOFree && i < C::kWorkFull))
-                count = 4;                       // the tile's softmax warps
-            else if (i >= C::kWorkFree && i < C::kNext)
-                count = 10;                      // two MMA threads, eight softmax warps
-            mbar_init(&bars[i], count);
-        }
+    if (tid < C::kNumBars) {
+        const int i = tid;
+        int count = 1;
+        if (i >= C::kFree && i < C::kSFull)
+            count = 2;                           // both tiles' MMA threads
+        else if ((i >= C::kPFull && i < C::kODone) || (i >= C::kOFree && i < C::kWorkFull))
+            count = 4;                           // the tile's softmax warps
+        else if (i >= C::kWorkFree && i < C::kNext)
+            count = 10;                          // two MMA threads, eight softmax warps
+        mbar_init(&bars[i], count);
         *abort_flag = 0;
+        *(abort_flag + 1) = 0;
         mbar_init_fence();
     }
     if (tid < 16)
@@ -198,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::prefetch_tmap(&qmap);
             tc::prefetch_tmap(&kmap);
             tc::prefetch_tmap(&vmap);
+            tc::prefetch_tmap(&omap);
             pdl_wait();
             auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
                 mbar_arrive_expect_tx(bar, C::kTileBytes);
@@ -213,9 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 Work w{0, -1, 0, 0};
                 if (block >= 0) {
-                    const int item = block / units;
+                    // items in the plan's order for chunk_units units of heads, then for the next ones
+                    const int chunk = block / (p.num_items * p.chunk_units), first = chunk * p.chunk_units;
+                    const int rest = block - p.num_items * first, width = min(p.chunk_units, units - first);
+                    const int item = rest / width;
                     const int32_t *it = p.items + (int64_t)item * kItemFields;
-                    w = Work{it[0], it[1], it[2], block - item * units};
+                    w = Work{it[0], it[1], it[2], first + rest - item * width};
                     if (w.row0 < 0 || w.len < 1 || w.len > p.num_rows - w.row0 || w.q0 < 0 || w.q0 >= w.len ||
                         w.q0 % kTile != 0) {
                         record_error(p.err, RLT_DEVERR_BAD_LEN);   // a plan of other sequences
@@ -334,6 +361,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else
                     mbar_arrive(&bars[bar]);
             };
+            // P V and the S behind it are issued as one: the two threads' MMAs would else alternate, both tiles' S
+            // would come at the same time, and both softmaxes would then want the same units at once.
+            volatile int *turn = abort_flag + 1;
+            auto take_turn = [&]() -> bool {
+                for (uint32_t it = 1; it != 0; ++it) {
+                    if (atomicCAS(const_cast<int *>(turn), 0, 1) == 0)
+                        return true;
+                    if ((it & 1023u) == 0u && *abort_flag != 0)
+                        return false;
+                }
+                return false;
+            };
+            auto pass_turn = [&]() { *turn = 0; };
             int tiles = 0, items = 0, s_issued = 0;   // key tiles and works with rows, over all works
             for (int d = 0;; ++d) {
                 if (!(ok = mbar_wait_or_abort(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag)))
@@ -367,6 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], tiles & 1u, abort_flag)))
                             break;
+                        if (!(ok = take_turn()))
+                            break;
                         tc::fence_after_sync();
                         issue_pv(0, v_slot, j == 0);
                         if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], tiles & 1u, abort_flag)))
@@ -383,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::mma_commit(&bars[C::kODone + s]);
                             ++items;
                         }
+                        pass_turn();
                     }
                     release(C::kFree + v_slot, j < ns);
                     if (j + 1 < n)
@@ -434,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t *bad = reinterpret_cast<uint32_t *>(base + C::kBadOff) + (d & 1) * 8;
             if (ns == 0 && lane == 0)
                 bad[s * 4 + quarter] = 0u;
-            float m_ref = -CUDART_INF_F, l_run = 0.f;
+            float m_ref = 0.f, l_run = 0.f;
             for (int j = 0; j < ns; ++j, ++tiles) {
                 if (j == ns - 1) {
                     // The tile of the row's own keys: weights of masked keys are 0, but 0 times an infinity or NaN
@@ -481,26 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = warp_wait(&bars[C::kSFull + s], tiles & 1u, abort_flag)))
                     break;
                 tc::fence_after_sync();
-                float v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc::tmem_ld32_nowait(t_s + c * 32, v[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tc::tmem_wait_ld(v[c]);
-                if (j == ns - 1) {                   // the diagonal: keys behind the query
-                    const int last = q_tok - j * kTile;
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i)
-                        v[i / 32][i % 32] = i <= last ? v[i / 32][i % 32] : -CUDART_INF_F;
-                }
-                // P = 2^(s - m), 32 columns at a time.  The first ones are made against the reference the row has,
-                // beside the row's maximum: it moves rarely, and then they are made again.  The exponentials
-                // of the next columns are issued ahead of the conversions of the last ones: the unit
-                // that makes them (8 lanes a clock) is what a warp waits for.
-                auto raise = [&](const float (&x)[32], float (&y)[32], float m) {
-                    const float m_sub = m == -CUDART_INF_F ? 0.f : m;
-                    const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_sub, -m_sub);
+                // P = 2^(s - m), 32 columns at a time.  The exponentials of the next columns are issued ahead of the
+                // conversions of the last ones.
+                uint64_t sum2[2] = {0ull, 0ull};
+                auto raise = [&](const float (&x)[32], float (&y)[32]) {
+                    const uint64_t sc2 = f2_pack(p.qscale, p.qscale), off2 = f2_pack(-m_ref, -m_ref);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 z = f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, off2));
@@ -508,7 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         y[2 * i + 1] = exp2_in_order(z.y);
                     }
                 };
-                uint64_t sum2[2] = {0ull, 0ull};
                 auto store = [&](const float (&y)[32], int c) {
                     uint32_t w[16];
 #pragma unroll
@@ -519,46 +546,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i)
                         sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(y[2 * i], y[2 * i + 1]));
                 };
-                float y0[32];
-                raise(v[0], y0, m_ref);
-                float mx4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                auto top = [&](float m, const float (&x)[32]) -> float {     // the larger of m and the columns', four chains
+                    float mx[4] = {m, x[0], x[1], x[2]};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mx4[k] = fmaxf(fmaxf(mx4[k], v[c][i + k]), v[c][i + 4 + k]);
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.qscale;
-                const bool up = mx > m_ref + kRescaleThreshold;
-                if (__any_sync(kFullMask, up)) {
+                    for (int i = 3; i < 31; i += 2)
+                        mx[(i >> 1) & 3] = fmaxf(fmaxf(mx[(i >> 1) & 3], x[i]), x[i + 1]);
+                    return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), x[31]);
+                };
+                // The reference moves up to the row's maximum where that exceeds it by 2^8, and O and the sum with it;
+                // the first tile sets it.  (S of this tile is behind the products of the last: O is at rest.)
+                auto move = [&](float mx, bool up) {
                     const float m_next = up ? mx : m_ref;
-                    const float scale_o = m_next == m_ref ? 1.f : fast_exp2(m_ref - m_next);
-                    if (j > 0) {                     // (S of this tile is behind the products of the last)
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            float o[16];
-                            uint32_t ow[16];
-                            tc::tmem_ld<16>(t_o + c * 16, o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                ow[i] = __float_as_uint(o[i] * scale_o);
-                            tc::tmem_st_nowait<16>(t_o + c * 16, ow);
-                        }
-                    }
-                    l_run *= scale_o;
+                    const float by = up ? fast_exp2(m_ref - m_next) : 1.f;
                     m_ref = m_next;
-                    raise(v[0], y0, m_ref);
+                    if (j == 0)
+                        return;
+                    l_run *= by;
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        uint32_t ow[16];
+                        tc::tmem_ld<16>(t_o + c * 16, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            ow[i] = __float_as_uint(o[i] * by);
+                        tc::tmem_st_nowait<16>(t_o + c * 16, ow);
+                    }
+                };
+                // (a row without a finite score keeps its reference; NaN scores stay NaN)
+                auto must_move = [&](float mx) -> bool {
+                    return mx > -CUDART_INF_F && (j == 0 || mx > m_ref + kRescaleThreshold);
+                };
+                if (j < ns - 1) {
+                    float v[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::tmem_ld32_nowait(t_s + c * 32, v[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::tmem_wait_ld(v[c]);
+                    // The first columns' weights are made against the reference the row has, beside the row's
+                    // maximum: it moves rarely, and then they are made again.
+                    float y0[32];
+                    raise(v[0], y0);
+                    const float mx = fmaxf(fmaxf(top(-CUDART_INF_F, v[0]), top(-CUDART_INF_F, v[1])),
+                                           fmaxf(top(-CUDART_INF_F, v[2]), top(-CUDART_INF_F, v[3]))) * p.qscale;
+                    if (__any_sync(kFullMask, must_move(mx))) {
+                        move(mx, must_move(mx));
+                        raise(v[0], y0);
+                    }
+                    raise(v[1], v[1]);
+                    store(y0, 0);
+                    raise(v[2], v[2]);
+                    store(v[1], 1);
+                    p_ready(0);                  // the first 64 keys' weights
+                    raise(v[3], v[3]);
+                    store(v[2], 2);
+                    store(v[3], 3);
+                    p_ready(1);
+                } else {
+                    // The row's own keys: a warp's rows see the 32 columns before its quarter whole, its quarter's up
+                    // to their own, and none behind, whose weights are zeros without an exponential.
+                    // Read twice, 32 columns at a time: P of columns c is stored over scores of columns c / 2.
+                    float mx = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int c = 0; c <= quarter; ++c) {
+                        float v[32];
+                        tc::tmem_ld32(t_s + c * 32, v);
+                        if (c == quarter) {
+#pragma unroll
+                            for (int i = 1; i < 32; ++i)
+                                v[i] = i <= lane ? v[i] : -CUDART_INF_F;
+                        }
+                        mx = top(mx, v);
+                    }
+                    mx *= p.qscale;
+                    if (__any_sync(kFullMask, must_move(mx)))
+                        move(mx, must_move(mx));
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if (c <= quarter) {
+                            float v[32];
+                            tc::tmem_ld32(t_s + c * 32, v);
+                            if (c == quarter) {
+#pragma unroll
+                                for (int i = 1; i < 32; ++i)
+                                    v[i] = i <= lane ? v[i] : -CUDART_INF_F;
+                            }
+                            raise(v, v);
+                            store(v, c);
+                        } else {
+                            tc::tmem_zero_nowait<16>(t_s + c * 16);
+                        }
+                        if (c & 1)
+                            p_ready(c >> 1);
+                    }
                 }
-                raise(v[1], v[1], m_ref);
-                store(y0, 0);
-                raise(v[2], v[2], m_ref);
-                store(v[1], 1);
-                p_ready(0);                          // the first 64 keys' weights
-                raise(v[3], v[3], m_ref);
-                store(v[2], 2);
-                store(v[3], 3);
-                p_ready(1);
                 const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
                 l_run += sum.x + sum.y;
             }
@@ -598,14 +681,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (q_tok < wk.len) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D);
+                // The warp's rows, 64 dims at a time, through shared memory and a tensor copy: a lane's row is a line of its
+                // own for every store instruction, and 8 warps' stores of that kind held up the shared-memory pipe (and
+                // with it every barrier of the CTA) for 2300 clocks a tile.  Rows at the end of a sequence are
+                // stored directly: the copy's box would reach into the next one's.
+                if (q_tok - lane + 31 < wk.len) {
+                    unsigned char *mine = base + C::kOutOff + warp * kOutBytes;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const float *x = &o[i / 4][i % 4 * 8];
-                        dst[i] = make_uint4(cvt_bf16x2(x[0] * inv, x[1] * inv), cvt_bf16x2(x[2] * inv, x[3] * inv),
-                                            cvt_bf16x2(x[4] * inv, x[5] * inv), cvt_bf16x2(x[6] * inv, x[7] * inv));
+                    for (int b = 0; b < kBlocks; ++b) {
+                        if (lane == 0)
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the last copy has read it
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float *x = &o[2 * b + c / 4][c % 4 * 8];
+                            *reinterpret_cast<uint4 *>(mine + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                                make_uint4(cvt_bf16x2(x[0] * inv, x[1] * inv), cvt_bf16x2(x[2] * inv, x[3] * inv),
+                                           cvt_bf16x2(x[4] * inv, x[5] * inv), cvt_bf16x2(x[6] * inv, x[7] * inv));
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tma_store_3d(&omap, mine, b * 64, head0 + s * head_step, wk.row0 + q_tok);
                     }
+                } else if (q_tok < wk.len) {
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const float *x = &o[i / 2][i % 2 * 16];
+                        uint32_t y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            y[k] = cvt_bf16x2(x[2 * k] * inv, x[2 * k + 1] * inv);
+                        store_sector(p.out + at * D + i * 16, y);
+                    }
+                }
+                if (q_tok < wk.len) {
                     if (p.lse_out != nullptr)
                         p.lse_out[at] = (m_ref + log2f(l_run)) * 0.6931471805599453f;
                 }
@@ -619,6 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok)
             *abort_flag = 1;
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");        // the output has left shared memory
     }
 
     tc::fence_before_sync();
@@ -630,12 +742,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// Token rows of `heads` x D bf16, `stride` elements apart; boxes of 128 tokens x 64 dims of one head.
-bool make_rows_map(CUtensorMap *map, const uint16_t *ptr, int64_t rows, int heads, int D, int64_t stride)
+// Token rows of `heads` x D bf16, `stride` elements apart; boxes of box_rows tokens x 64 dims of one head.
+bool make_rows_map(CUtensorMap *map, const uint16_t *ptr, int64_t rows, int heads, int D, int64_t stride,
+                   int box_rows = kTile)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, kTile};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     const tc::EncodeTiledFn fn = tc::encode_tiled_fn();
     return fn != nullptr && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(ptr), dims, strides, box,
@@ -648,10 +761,11 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
 {
     using C = PCfg<D>;
     static_assert(C::kSmem <= 227 * 1024, "shared memory of one CTA");
-    CUtensorMap qmap, kmap, vmap;
+    CUtensorMap qmap, kmap, vmap, omap;
     if (!make_rows_map(&qmap, p.q, p.num_rows, p.num_q_heads, D, p.q_stride) ||
         !make_rows_map(&kmap, p.k, p.num_rows, p.num_kv_heads, D, p.k_stride) ||
-        !make_rows_map(&vmap, p.v, p.num_rows, p.num_kv_heads, D, p.v_stride))
+        !make_rows_map(&vmap, p.v, p.num_rows, p.num_kv_heads, D, p.v_stride) ||
+        !make_rows_map(&omap, p.out, p.num_rows, p.num_q_heads, D, (int64_t)p.num_q_heads * D, 32))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
@@ -665,10 +779,20 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
             return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    const int G = p.num_q_heads / p.num_kv_heads;
-    const unsigned units = G % 2 == 0 ? p.num_q_heads / 2 : p.num_q_heads;
-    return launch_kernel(prefill_kernel<D>, dim3(p.num_items * units), dim3(kThreads), C::kSmem, stream, early, qmap,
-                         kmap, vmap, p);
+    // The items of a unit re-read its kv head's rows.  Where the rows of all kv heads overflow L2, and the largest
+    // item is small beside an SM's share of the work (the order by size then starts anew a few times), as
+    // many kv heads run through the plan at a time as keep theirs in L2.  16 prompts of 1024-2000 tokens, 32 kv
+    // heads, 400 MB of K and V: 299 us in parts, 318 in one; one prompt of 2048 tokens, 128 kv heads: 131
+    // in parts, 123 in one (an item is a quarter of an SM's share there).
+    const int G = p.num_q_heads / p.num_kv_heads, per_kv = G % 2 == 0 ? G / 2 : G;
+    const int64_t kv_bytes = (int64_t)p.num_rows * D * 4;
+    int64_t kv_heads = std::min<int64_t>(std::max<int64_t>(kL2Share / kv_bytes, 1), p.num_kv_heads);
+    if ((int64_t)p.total_tiles * per_kv * p.num_kv_heads < (int64_t)kPartsFrom * p.num_sms * p.max_tiles)
+        kv_heads = p.num_kv_heads;
+    PrefillParams c = p;
+    c.chunk_units = (int32_t)kv_heads * per_kv;
+    return launch_kernel(prefill_kernel<D>, dim3(p.num_items * per_kv * p.num_kv_heads), dim3(kThreads), C::kSmem,
+                         stream, early, qmap, kmap, vmap, omap, c);
 }
 
 }  // namespace
@@ -689,18 +813,23 @@ extern "C" RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t 
         (max_items > 0 && items == nullptr))
         return RLT_ERR_INVALID_ARG;
     const int64_t step = query_group % 2 == 0 ? 128 : 256;
-    int64_t rows = 0, count = 0, longest = 0;
+    int64_t rows = 0, count = 0, longest = 0, tiles = 0;
     for (int32_t b = 0; b < batch; ++b) {
         if (seq_lens[b] < 0)
             return RLT_ERR_INVALID_ARG;
         rows += seq_lens[b];
         count += (seq_lens[b] + step - 1) / step;
+        const int64_t all = (seq_lens[b] + 127) / 128;           // key tiles of the items: step/128, 2 step/128, ..
+        for (int64_t n = step / 128; n < all + step / 128; n += step / 128)
+            tiles += std::min(n, all);
         longest = std::max<int64_t>(longest, seq_lens[b]);
     }
     if (rows > INT32_MAX)
         return RLT_ERR_UNSUPPORTED;
     sizes[0] = (int32_t)count;
     sizes[1] = (int32_t)rows;
+    sizes[2] = (int32_t)((longest + 127) / 128);
+    sizes[3] = (int32_t)std::min<int64_t>(tiles, INT32_MAX);
     if (count > max_items)
         return RLT_ERR_OUT_OF_RANGE;
     // The items with the most keys first, so that the grid ends on short ones: from the longest

@@ -235,6 +235,9 @@ struct PrefillParams {
     float *lse_out;              // [num_rows][num_q_heads] or null
     unsigned int *err;
     int32_t num_rows, num_items, num_q_heads, num_kv_heads;
+    int32_t max_tiles, total_tiles;   // key tiles of the plan's largest item and of all items
+    int32_t num_sms;
+    int32_t chunk_units;         // units of heads that run through the items together (launch_prefill sets it)
     float qscale;                // softmax scale * log2(e)
 };
 

@@ -89,19 +89,20 @@ def test_decode_of_nothing(lib):
 
 
 def prefill(lib, **kw):
-    f = dict(q=A, hq=4, qs=512, k=A * 2, ks=256, v=A * 3, vs=256, hkv=2, d=128, n=300, items=A * 4, ni=3, scale=0.0,
+    f = dict(q=A, hq=4, qs=512, k=A * 2, ks=256, v=A * 3, vs=256, hkv=2, d=128, n=300, items=A * 4, ni=3, mt=3, tt=6, scale=0.0,
              out=A * 5, lse=A * 6, flags=0)
     f.update(kw)
     return lib.rlt_prefill_attn(f["q"], f["hq"], f["qs"], f["k"], f["ks"], f["v"], f["vs"], f["hkv"], f["d"], f["n"],
-                                f["items"], f["ni"], f["scale"], f["out"], f["lse"], f["flags"], 0)
+                                f["items"], f["ni"], f["mt"], f["tt"], f["scale"], f["out"], f["lse"], f["flags"], 0)
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(flags=4), INVALID), (dict(n=-1), INVALID), (dict(ni=-1), INVALID), (dict(hkv=0), INVALID), (dict(hq=5), INVALID),
+    (dict(flags=4), INVALID), (dict(n=-1), INVALID), (dict(ni=-1), INVALID), (dict(mt=-1), INVALID), (dict(tt=-1), INVALID), (dict(hkv=0), INVALID), (dict(hq=5), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(d=96), UNSUPPORTED), (dict(ni=1 << 30), UNSUPPORTED), (dict(n=0), INVALID),
     (dict(q=0), INVALID), (dict(v=0), INVALID), (dict(items=0), INVALID), (dict(out=0), INVALID), (dict(k=A + 2), INVALID),
     (dict(items=A + 2), INVALID), (dict(lse=A + 1), INVALID), (dict(qs=256), INVALID), (dict(ks=260), INVALID),
-    (dict(out=A), INVALID), (dict(out=A * 2 - 1024), INVALID)])
+    (dict(out=A), INVALID), (dict(out=A * 2 - 1024), INVALID),
+    (dict(out=A * 5 + 16), INVALID)])
 def test_prefill_refusals(lib, change, status):
     assert prefill(lib, **change) == status
 
@@ -126,12 +127,14 @@ def test_prefill_plan(lib, group, step):
         rlt.rlt_plan_prefill([1 << 30, 1 << 30], group)
     with pytest.raises(rlt.RltError):
         rlt.rlt_plan_prefill([5], 0)
-    sizes = np.zeros(2, np.int32)
+    tiles = [-(-min(q0 + step, n) // 128) for _, n, q0, _ in want]
+    assert plan.max_key_tiles == max(tiles) and plan.total_key_tiles == sum(tiles)
+    sizes = np.zeros(4, np.int32)
     sl = np.array(lens, np.int32)
     items = np.zeros((1, 4), np.int32)
     p = lambda a: a.ctypes.data_as(ctypes.c_void_p)              # noqa: E731
     assert lib.rlt_plan_prefill(p(sl), len(lens), group, p(items), 1, p(sizes)) == RANGE
-    assert sizes.tolist() == [len(want), sum(lens)]
+    assert sizes.tolist() == [len(want), sum(lens), max(tiles), sum(tiles)]
 
 
 def test_reference_number_format():
