@@ -620,7 +620,9 @@ class KV8Pool:
                             ("k_exp", k_exp, torch.uint8), ("v_exp", v_exp, torch.uint8)):
             _dev(t, dt, name)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.device = _same_device(k, v, k_exp, v_exp)
+        self.device_index = k.get_device()
+        if any(t.get_device() != self.device_index for t in (v, k_exp, v_exp)):
+            raise ValueError("the pool's tensors must be on one device")
         nb, P, Hkv, ps, D = k.shape
         self.num_banks, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = nb, P, Hkv, ps, D
         self.struct = rlt_kv8_pool(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), P, nb, Hkv, ps, D)
@@ -635,16 +637,10 @@ class KV8Pool:
                    *(torch.empty(shape[:4], dtype=torch.uint8, device=device) for _ in range(2)))
 
 
-def _same_device(*tensors):
-    """The index of these tensors' device (None entries aside); they must share it, and it must be the current one:
-    the library launches on the current device."""
+def _device_index():
+    """Index of the current device: the library launches there, so every tensor of a call has to be there."""
     import torch
-    found = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != found:
-            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{found}: "
-                             "all tensors of a call must be on the current device")
-    return found
+    return torch._C._cuda_getDevice()
 
 
 def _record(stream, *made):
@@ -659,28 +655,56 @@ def _record(stream, *made):
             t.record_stream(s)
 
 
-def _token_rows(t, heads, D, n, name):
-    """(pointer, token stride) of bf16 [n][heads][D] rows whose heads are contiguous (a view of a fused projection)."""
+def _refuse(t, dtype, name, shape, dev):
+    """Says what keeps t from being a tensor of this type and shape on the current device."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    if t.shape != (n, heads, D):
-        raise ValueError(f"{name} must be [tokens][heads][head_dim] = {(n, heads, D)}, got {tuple(t.shape)}")
-    stride = t.stride()
-    if n > 0 and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}: all tensors of a call "
+                         "must be on the current device")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _token_rows(t, dtype, shape, name, dev):
+    """(pointer, token stride) of rows [n][heads][D] whose heads are contiguous (a view of a fused projection)."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, dtype, name, shape, dev)
+    n, heads, D = shape
+    s0, s1, s2 = t.stride()
+    if n > 0 and (s2 != 1 or (heads > 1 and s1 != D)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (stride[0] if n > 1 else heads * D)
+    return t.data_ptr(), (s0 if n > 1 else heads * D)
 
 
-def _ptr(t, dtype, name, shape=None):
+def _ptr(t, dtype, shape, name, dev):
     """Device address of a contiguous tensor of this type and shape, or 0 for None."""
     if t is None:
         return 0
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _dev(t, dtype, name)                                    # says what is wrong
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(t, dtype, name, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a contiguous workspace tensor of any type, or (0, 0)."""
+    if ws is None:
+        return 0, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on the current device cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def rlt_kv8_append_rope(pool: KV8Pool, bank: int, k_new, v_new, positions, out_loc, rot_dim: int, rope_base: float,
@@ -690,32 +714,36 @@ def rlt_kv8_append_rope(pool: KV8Pool, bank: int, k_new, v_new, positions, out_l
     the entry).  q_out: the rotated queries (made if q is given without it: zeros where an entry is skipped);
     k_out / v_out (optional): bf16 [N][Hkv][D], the rows as the pool holds them.  Returns q_out (None without q)."""
     import torch
-    n, Hkv, D = int(out_loc.numel()), pool.num_kv_heads, pool.head_dim
-    kp, ks = _token_rows(k_new, Hkv, D, n, "k_new")
-    vp, vs = _token_rows(v_new, Hkv, D, n, "v_new")
+    bf16, i64, dev = torch.bfloat16, torch.int64, _device_index()
+    n, Hkv, D = out_loc.numel(), pool.num_kv_heads, pool.head_dim
+    kp, ks = _token_rows(k_new, bf16, (n, Hkv, D), "k_new", dev)
+    vp, vs = _token_rows(v_new, bf16, (n, Hkv, D), "v_new", dev)
     Hq, qp, qs = 0, 0, 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [tokens][heads][head_dim]")
-        Hq = int(q.shape[1])
-        qp, qs = _token_rows(q, Hq, D, n, "q")
+        Hq = q.shape[1]
+        qp, qs = _token_rows(q, bf16, (n, Hq, D), "q", dev)
         if q_out is None:
-            q_out = torch.zeros((n, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.zeros((n, Hq, D), dtype=bf16, device=q.device)
             _record(stream, q_out)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(pool.k, k_new, v_new, positions, out_loc, q, q_out, k_out, v_out, request, written)
-    batch = 0
+    if pool.device_index != dev:
+        raise ValueError(f"the pool is on cuda:{pool.device_index}, but the current device is cuda:{dev}")
+    batch, wp, rp = 0, 0, 0
     if written is not None:
         if written.dim() != 2 or written.shape[0] != pool.num_banks or request is None:
             raise ValueError("written must be [num_banks][batch] and needs request")
         batch = int(written.shape[1])
+        wp = _ptr(written, torch.int32, written.shape, "written", dev)
+        rp = _ptr(request, torch.int32, (n,), "request", dev)
+    held = (n, Hkv, D)
     _check(load().rlt_kv8_append_rope(
-        pool.ref, bank, qp, Hq, qs, kp, ks, vp, vs, _ptr(positions, torch.int64, "positions", (n,)),
-        _ptr(out_loc, torch.int64, "out_loc", (n,)), n, int(rot_dim), float(rope_base),
-        _ptr(q_out, torch.bfloat16, "q_out", (n, Hq, D)), _ptr(k_out, torch.bfloat16, "k_out", (n, Hkv, D)),
-        _ptr(v_out, torch.bfloat16, "v_out", (n, Hkv, D)), _ptr(request, torch.int32, "request", (n,)),
-        _ptr(written, torch.int32, "written"), batch, _stream(stream)), "rlt_kv8_append_rope")
+        pool.ref, bank, qp, Hq, qs, kp, ks, vp, vs, _ptr(positions, i64, (n,), "positions", dev),
+        _ptr(out_loc, i64, (n,), "out_loc", dev), n, int(rot_dim), float(rope_base), _ptr(q_out, bf16, (n, Hq, D), "q_out", dev),
+        _ptr(k_out, bf16, held, "k_out", dev), _ptr(v_out, bf16, held, "v_out", dev), rp, wp, batch,
+        _raw_stream(stream, dev)), "rlt_kv8_append_rope")
     return q_out
 
 
@@ -730,25 +758,29 @@ def rlt_paged_decode_attn_kv8(pool: KV8Pool, bank: int, q, page_table, seq_lens,
                               early_start: bool = False):
     """Paged decode attention over one bank of an 8-bit pool; arguments as rlt_paged_decode_attn."""
     import torch
-    _check_q_out(pool, q, out, lse_out)
-    B, Hq, D = q.shape
-    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("page_table must be [B][max_pages] and seq_lens [B]")
+    bf16, i32, dev = torch.bfloat16, torch.int32, _device_index()
+    if q.dim() != 3 or q.shape[2] != pool.head_dim:
+        raise ValueError(f"q must be [B][Hq][head_dim] with the pool's head_dim {pool.head_dim}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    if pool.device_index != dev:
+        raise ValueError(f"the pool is on cuda:{pool.device_index}, but the current device is cuda:{dev}")
+    shape = q.shape
+    B, Hq, D = shape
+    pages = page_table.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty(shape, dtype=bf16, device=q.device)
         _record(stream, out)
     if workspace is None:
         need = rlt_paged_decode_kv8_workspace_size(B, Hq, pool.num_kv_heads, D, max_seq_len, split_tokens)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 0 else None
         _record(stream, workspace)
-    _same_device(pool.k, q, page_table, seq_lens, out, lse_out, workspace)
+    wp, wbytes = _workspace(workspace, dev)
     _check(load().rlt_paged_decode_attn_kv8(
-        pool.ref, bank, _ptr(q, torch.bfloat16, "q"), Hq, _ptr(page_table, torch.int32, "page_table"),
-        page_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), B, int(max_seq_len), float(scale),
-        _ptr(out, torch.bfloat16, "out"), _ptr(lse_out, torch.float32, "lse_out"),
-        workspace.data_ptr() if workspace is not None else 0,
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, int(split_tokens),
-        ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_paged_decode_attn_kv8")
+        pool.ref, bank, _ptr(q, bf16, shape, "q", dev), Hq, _ptr(page_table, i32, (B, pages), "page_table", dev), pages,
+        _ptr(seq_lens, i32, (B,), "seq_lens", dev), B, int(max_seq_len), float(scale), _ptr(out, bf16, shape, "out", dev),
+        _ptr(lse_out, torch.float32, (B, Hq), "lse_out", dev), wp, wbytes, int(split_tokens),
+        ATTN_EARLY_START if early_start else 0, _raw_stream(stream, dev)), "rlt_paged_decode_attn_kv8")
     return out
 
 
@@ -792,13 +824,15 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
     allowed), N >= the plan's rows; rows behind the last sequence are left alone (zeros in an out made here).
     Returns out [N][Hq][D]."""
     import torch
+    bf16, dev = torch.bfloat16, _device_index()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [tokens][heads][head_dim]")
-    N, Hq, D = q.shape
-    Hkv = int(k.shape[1])
-    qp, qs = _token_rows(q, Hq, D, N, "q")
-    kp, ks = _token_rows(k, Hkv, D, N, "k")
-    vp, vs = _token_rows(v, Hkv, D, N, "v")
+    shape = q.shape
+    N, Hq, D = shape
+    Hkv = k.shape[1]
+    qp, qs = _token_rows(q, bf16, shape, "q", dev)
+    kp, ks = _token_rows(k, bf16, (N, Hkv, D), "k", dev)
+    vp, vs = _token_rows(v, bf16, (N, Hkv, D), "v", dev)
     if N < plan.num_rows:
         raise ValueError("the plan was built for more rows")
     if plan.num_items and plan.query_group * Hkv != Hq:
@@ -806,12 +840,11 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
     if plan.dev is None:
         plan.to(q.device)
     if out is None:
-        out = (torch.empty if N == plan.num_rows else torch.zeros)((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = (torch.empty if N == plan.num_rows else torch.zeros)(shape, dtype=bf16, device=q.device)
         _record(stream, out)
-    _same_device(q, k, v, plan.dev, out, lse_out)
     _check(load().rlt_prefill_attn(
-        qp, Hq, qs, kp, ks, vp, vs, Hkv, D, N, _ptr(plan.dev, torch.int32, "plan"), plan.num_items,
-        plan.max_key_tiles, plan.total_key_tiles, float(scale),
-        _ptr(out, torch.bfloat16, "out", (N, Hq, D)), _ptr(lse_out, torch.float32, "lse_out", (N, Hq)),
-        ATTN_EARLY_START if early_start else 0, _stream(stream)), "rlt_prefill_attn")
+        qp, Hq, qs, kp, ks, vp, vs, Hkv, D, N, _ptr(plan.dev, torch.int32, plan.dev.shape, "plan", dev), plan.num_items,
+        plan.max_key_tiles, plan.total_key_tiles, float(scale), _ptr(out, bf16, shape, "out", dev),
+        _ptr(lse_out, torch.float32, (N, Hq), "lse_out", dev), ATTN_EARLY_START if early_start else 0,
+        _raw_stream(stream, dev)), "rlt_prefill_attn")
     return out
