@@ -103,9 +103,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8], float by)
 // Rotations whose halves are whole 16-byte chunks (rot_dim a multiple of 16; so is head_dim).  A lane holds the
 // two chunks of a row that turn into each other (or two neighbouring chunks behind rot_dim) and D / 16
 // lanes a row, so a row needs no exchange but its largest magnitude.  A warp stays with one token: its
-// angles are computed once and used for every head; the rows of kBatch rounds are loaded before
-// the first is worked on.  Bound by memory: 2 (hq + 2 hkv) D bytes in, as many out, and the cache.
-constexpr int kBatch = 4;
+// angles are computed once and used for every head; the rows of kBatch rounds are loaded before the
+// first is worked on.  Bound by memory: 2 (hq + 2 hkv) D bytes in, as many out, and the cache.
+constexpr int kBatch = 3;
 
 template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(const Kv8AppendParams p, int splits)
@@ -117,22 +117,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(co
     if (i >= p.n_tokens)
         return;
     const int part = (int)(w - i * splits);
-    const int64_t slot = token_slot(p, i, part == 0 && lane == 0);
-    if (slot < 0)
-        return;
     const int t = lane % kLanes, r0 = part * kRows + lane / kLanes, step = splits * kRows;
+    __shared__ __align__(16) float2 angles[kAppendWarps][64];
+    float2 *mine = angles[threadIdx.x >> 5];
     const int turned = p.rot_dim / 16;
     const bool turns = t < turned;
     const int ca = turns ? t : 2 * t, cb = turns ? t + turned : 2 * t + 1;   // this lane's chunks
     const int heads = p.num_q_heads + 2 * p.num_kv_heads;
 
-    float c[8], s[8];
-    const uint64_t pos = turns ? (uint64_t)p.positions[i] : 0ull;
-    bool angles = false;
-    const int64_t page = slot / p.page_size;
-    const int64_t at0 = page * p.num_kv_heads * p.page_size + (slot - page * p.page_size);
-    for (int r = r0; r - r0 < heads - part * kRows; r += step * kBatch) {   // (uniform over the warp)
-        uint4 a[kBatch], b[kBatch];
+    uint4 a[kBatch], b[kBatch];
+    auto load = [&](int r) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = r + u * step;
@@ -144,15 +138,30 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(co
                 a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        if (!angles) {                           // while the first rows are on their way
-            angles = true;
+    };
+    const uint64_t pos = turned > 0 ? (uint64_t)p.positions[i] : 0ull;
+    load(r0);                                    // (rows of an unused entry are read too: one round trip fewer)
+    const int64_t slot = token_slot(p, i, part == 0 && lane == 0);
+    if (slot < 0)
+        return;
+    // A lane makes at most two of the token's rot_dim / 2 angles and takes its eight from the warp's.
+    float c[8], s[8];
+    for (int k = lane; k < p.rot_dim / 2; k += 32)
+        turn_cos_sin(pos * p.freq[k], mine[k].x, mine[k].y);
+    __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                c[k] = s[k] = 0.f;
-                if (turns)
-                    turn_cos_sin(pos * p.freq[t * 8 + k], c[k], s[k]);
-            }
-        }
+    for (int k = 0; k < 8; k += 2) {
+        const float4 x = turns ? *reinterpret_cast<const float4 *>(&mine[t * 8 + k]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        c[k] = x.x;
+        s[k] = x.y;
+        c[k + 1] = x.z;
+        s[k + 1] = x.w;
+    }
+    const int64_t page = slot / p.page_size;
+    const int64_t at0 = page * p.num_kv_heads * p.page_size + (slot - page * p.page_size);
+    for (int r = r0; r - r0 < heads - part * kRows; r += step * kBatch) {   // (uniform over the warp)
+        if (r != r0)
+            load(r);
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = r + u * step;
@@ -214,13 +223,34 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(co
     }
 }
 
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *src, uint32_t (&x)[N])
+{
+    if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(src);
+        x[0] = v.x;
+        x[1] = v.y;
+    } else {
+        x[0] = *src;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_words(uint16_t *row, int lane, const uint32_t (&y)[N])
+{
+    if constexpr (N == 2)
+        reinterpret_cast<uint2 *>(row)[lane] = make_uint2(y[0], y[1]);
+    else
+        reinterpret_cast<uint32_t *>(row)[lane] = y[0];
+}
+
 // Any even rot_dim: a row passes through shared memory, where a lane finds the other member of its pairs.
 // A warp stays with one token; its angles (at most two pairs a lane) are computed once.
 template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(const Kv8AppendParams p, int splits)
 {
     constexpr int kWords = D / 64;               // 32-bit words of a row that a lane loads
-    __shared__ float rows[kAppendWarps][D];
+    __shared__ __align__(16) float rows[kAppendWarps][kBatch][D];
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int64_t i = w / splits;
@@ -230,7 +260,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(con
     const int64_t slot = token_slot(p, i, part == 0 && lane == 0);
     if (slot < 0)
         return;
-    float *row = rows[threadIdx.x >> 5];
+    float (*row)[D] = rows[threadIdx.x >> 5];
     const int heads = p.num_q_heads + 2 * p.num_kv_heads;
     float c[2], s[2];
 #pragma unroll
@@ -239,65 +269,90 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(con
             turn_cos_sin((uint64_t)p.positions[i] * p.freq[lane + 32 * k], c[k], s[k]);
     const int64_t page = slot / p.page_size;
     const int64_t at0 = page * p.num_kv_heads * p.page_size + (slot - page * p.page_size);
-    uint32_t next[kWords];
-    auto load = [&](int h) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(row_at(p, i, h, D).src) + lane * kWords;
+    for (int h0 = part; h0 < heads; h0 += splits * kBatch) {
+        uint32_t x[kBatch][kWords];
 #pragma unroll
-        for (int k = 0; k < kWords; ++k)
-            next[k] = src[k];
-    };
-    if (part < heads)
-        load(part);
-    for (int h = part; h < heads; h += splits) {
-        const RowAt r = row_at(p, i, h, D);
-        uint32_t amax = 0u;
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-            const uint32_t x = next[k];
-            amax = max(amax, max(x & 0x7fffu, (x >> 16) & 0x7fffu));
-            *reinterpret_cast<float2 *>(row + (lane * kWords + k) * 2) = make_float2(bf16_lo(x), bf16_hi(x));
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = min(h0 + u * splits, heads - 1);       // (a row past the last is loaded, not written)
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(row_at(p, i, h, D).src) + lane * kWords;
+            load_words(src, x[u]);
         }
-        if (h + splits < heads)
-            load(h + splits);
-        amax = __reduce_max_sync(kFullMask, amax);
         __syncwarp();
-        if (r.kind < 2) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if constexpr (kWords == 2)
+                *reinterpret_cast<float4 *>(row[u] + lane * 4) =
+                    make_float4(bf16_lo(x[u][0]), bf16_hi(x[u][0]), bf16_lo(x[u][1]), bf16_hi(x[u][1]));
+            else
+                *reinterpret_cast<float2 *>(row[u] + lane * 2) = make_float2(bf16_lo(x[u][0]), bf16_hi(x[u][0]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (h0 + u * splits >= p.num_q_heads + p.num_kv_heads)
+                break;                           // values
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int j = lane + 32 * k;
                 if (j < half) {
-                    const float x = row[j], y = row[j + half];
-                    row[j] = fmaf(x, c[k], -(y * s[k]));
-                    row[j + half] = fmaf(y, c[k], x * s[k]);
+                    const float a = row[u][j], b = row[u][j + half];
+                    row[u][j] = fmaf(a, c[k], -(b * s[k]));
+                    row[u][j + half] = fmaf(b, c[k], a * s[k]);
                 }
             }
-            __syncwarp();
         }
-        const uint32_t byte = row_exponent(amax);
-        const float scale = exp_scale(byte), inv = exp_inverse(byte);
-        const int64_t at = at0 + (int64_t)r.g * p.page_size;
-        uint16_t *held = r.kind == 1 ? p.k_out : p.v_out;
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-            const int d = (lane * kWords + k) * 2;
-            const float2 f = *reinterpret_cast<const float2 *>(row + d);
+        for (int u = 0; u < kBatch; ++u) {
+            const int h = h0 + u * splits;
+            if (h >= heads)
+                break;
+            const RowAt r = row_at(p, i, h, D);
+            uint32_t amax = 0u;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k)
+                amax = max(amax, max(x[u][k] & 0x7fffu, (x[u][k] >> 16) & 0x7fffu));
+            if (r.kind != 0)
+                amax = __reduce_max_sync(kFullMask, amax);
+            const uint32_t byte = row_exponent(amax);
+            const float scale = exp_scale(byte), inv = exp_inverse(byte);
+            const int64_t at = at0 + (int64_t)r.g * p.page_size;
+            uint16_t *held = r.kind == 1 ? p.k_out : p.v_out;
+            float f[2 * kWords];
+            if constexpr (kWords == 2) {
+                const float4 v = *reinterpret_cast<const float4 *>(row[u] + lane * 4);
+                f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(row[u] + lane * 2);
+                f[0] = v.x; f[1] = v.y;
+            }
+            uint32_t y[kWords], x8 = 0u;
             if (r.kind == 0) {
-                *reinterpret_cast<uint32_t *>(p.q_out + (i * p.num_q_heads + r.g) * D + d) = cvt_bf16x2(f.x, f.y);
+#pragma unroll
+                for (int k = 0; k < kWords; ++k)
+                    y[k] = cvt_bf16x2(f[2 * k], f[2 * k + 1]);
+                store_words(p.q_out + (i * p.num_q_heads + r.g) * D, lane, y);
                 continue;
             }
-            const uint32_t x8 = e4m3x2(f.x * inv, f.y * inv);
-            *reinterpret_cast<uint16_t *>((r.kind == 1 ? p.k_bank : p.v_bank) + at * D + d) = (uint16_t)x8;
-            if (held != nullptr) {
-                const float2 v = f32x2_of_f16(f16x2_of_e4m3(x8));
-                *reinterpret_cast<uint32_t *>(held + (i * p.num_kv_heads + r.g) * D + d) =
-                    cvt_bf16x2(v.x * scale, v.y * scale);
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                const uint32_t pair = e4m3x2(f[2 * k] * inv, f[2 * k + 1] * inv);
+                const float2 v = f32x2_of_f16(f16x2_of_e4m3(pair));
+                y[k] = cvt_bf16x2(v.x * scale, v.y * scale);
+                x8 |= pair << (16 * k);
             }
-        }
-        if (r.kind != 0 && lane == 0) {
-            (r.kind == 1 ? p.k_exp : p.v_exp)[at] = (uint8_t)byte;
-            if (r.kind == 1 && r.g == 0 && p.written != nullptr)
-                count_written(p, i);
+            uint8_t *dst = (r.kind == 1 ? p.k_bank : p.v_bank) + at * D;
+            if constexpr (kWords == 2)
+                reinterpret_cast<uint32_t *>(dst)[lane] = x8;
+            else
+                reinterpret_cast<uint16_t *>(dst)[lane] = (uint16_t)x8;
+            if (held != nullptr)
+                store_words(held + (i * p.num_kv_heads + r.g) * D, lane, y);
+            if (lane == 0) {
+                (r.kind == 1 ? p.k_exp : p.v_exp)[at] = (uint8_t)byte;
+                if (r.kind == 1 && r.g == 0 && p.written != nullptr)
+                    count_written(p, i);
+            }
         }
     }
 }
