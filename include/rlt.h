@@ -550,7 +550,7 @@ typedef struct rlt_kv8_pool {
  *                    before the one rounding to bf16 or e4m3
  *   request, written, batch  as rlt_kv_append_rope
  * An output may be the call's own input of the same kind (same address, rows
- * num_heads*head_dim apart); any other overlap is RLT_ERR_INVALID_ARG.  All arrays but
+ * num_heads*head_dim apart); any other overlap, also with the pool, is RLT_ERR_INVALID_ARG.  All arrays but
  * positions, out_loc, request and written (their elements' alignment) 16-byte aligned.
  */
 RLT_API rlt_status rlt_kv8_append_rope(const rlt_kv8_pool *pool, int32_t bank, const void *q, int32_t num_q_heads,
@@ -608,7 +608,9 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
  *   lse_out    fp32 [num_rows][num_q_heads], natural log, or NULL
  *   flags      0 or RLT_ATTN_EARLY_START (no kernel still running ahead may write items)
  * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
- * fp32, weights enter the product with V as bf16.
+ * fp32; weights enter the product with V as bf16, up to 2^8 (values up to 2^119 cannot
+ * overflow by it).  An infinity or NaN in q, k or v reaches the rows whose formula it is
+ * part of and no other: not earlier rows, not other sequences.
  */
 RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t batch, int32_t query_group, int32_t *items,
                                     int32_t max_items, int32_t *sizes);

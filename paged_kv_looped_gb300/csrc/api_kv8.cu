@@ -91,6 +91,14 @@ RLT_API rlt_status rlt_kv8_append_rope(const rlt_kv8_pool *pool, int32_t bank, c
             if (clashes(out[o], in[i], o == i) || (i < o && clashes(out[o], out[i], false)))
                 return RLT_ERR_INVALID_ARG;
     const int64_t slots = pool->num_pages * pool->page_size;
+    // nor on the pool's own arrays (in 2-byte elements, rounded up)
+    const int64_t pool_rows = (int64_t)pool->num_banks * slots * pool->num_kv_heads;
+    const Block held[4] = {{pool->k, 1, pool_rows * pool->head_dim / 2, 0}, {pool->v, 1, pool_rows * pool->head_dim / 2, 0},
+                           {pool->k_exp, 1, (pool_rows + 1) / 2, 0}, {pool->v_exp, 1, (pool_rows + 1) / 2, 0}};
+    for (int o = 0; o < 3; ++o)
+        for (int i = 0; i < 4; ++i)
+            if (clashes(out[o], held[i], false))
+                return RLT_ERR_INVALID_ARG;
     if ((st = rlt::validate_slots(out_loc, n_tokens, slots, static_cast<cudaStream_t>(stream))) != RLT_OK)
         return st;
 

@@ -175,6 +175,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int units = pair ? p.num_q_heads / 2 : p.num_q_heads;
     const int head_step = pair ? 1 : 0, tok_step = pair ? 0 : kTile;
 
+    // The load warp's first round trips go out before the CTA is set up: the maps, and the first work's item.
+    auto find = [&](int block) -> Work {
+        // items in the plan's order for chunk_units units of heads, then for the next ones
+        const int chunk = block / (p.num_items * p.chunk_units), first = chunk * p.chunk_units;
+        const int rest = block - p.num_items * first, width = min(p.chunk_units, units - first);
+        const int item = rest / width;
+        const int32_t *it = p.items + (int64_t)item * kItemFields;
+        return Work{it[0], it[1], it[2], first + rest - item * width};
+    };
+    Work first_work{0, 0, 0, 0};
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            tc::prefetch_tmap(&qmap);
+            tc::prefetch_tmap(&kmap);
+            tc::prefetch_tmap(&vmap);
+            tc::prefetch_tmap(&omap);
+        }
+        first_work = find(blockIdx.x);
+    }
     if (tid < C::kNumBars) {
         const int i = tid;
         int count = 1;
@@ -218,10 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // them: the items keep their order, and a CTA's start is paid once.  The next work is asked
             // for while this one's copies are issued.  Ring order K0, V0, K1, V1, ...; rows behind
             // the last one of the array read as zeros.
-            tc::prefetch_tmap(&qmap);
-            tc::prefetch_tmap(&kmap);
-            tc::prefetch_tmap(&vmap);
-            tc::prefetch_tmap(&omap);
             pdl_wait();
             auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
                 mbar_arrive_expect_tx(bar, C::kTileBytes);
@@ -237,12 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 Work w{0, -1, 0, 0};
                 if (block >= 0) {
-                    // items in the plan's order for chunk_units units of heads, then for the next ones
-                    const int chunk = block / (p.num_items * p.chunk_units), first = chunk * p.chunk_units;
-                    const int rest = block - p.num_items * first, width = min(p.chunk_units, units - first);
-                    const int item = rest / width;
-                    const int32_t *it = p.items + (int64_t)item * kItemFields;
-                    w = Work{it[0], it[1], it[2], first + rest - item * width};
+                    w = d == 0 ? first_work : find(block);
                     if (w.row0 < 0 || w.len < 1 || w.len > p.num_rows - w.row0 || w.q0 < 0 || w.q0 >= w.len ||
                         w.q0 % kTile != 0) {
                         record_error(p.err, RLT_DEVERR_BAD_LEN);   // a plan of other sequences
@@ -478,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ns == 0 && lane == 0)
                 bad[s * 4 + quarter] = 0u;
             float m_ref = 0.f, l_run = 0.f;
+            bool m_set = false;
             for (int j = 0; j < ns; ++j, ++tiles) {
                 if (j == ns - 1) {
                     // The tile of the row's own keys: weights of masked keys are 0, but 0 times an infinity or NaN
@@ -554,11 +565,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), x[31]);
                 };
                 // The reference moves up to the row's maximum where that exceeds it by 2^8, and O and the sum with it;
-                // the first tile sets it.  (S of this tile is behind the products of the last: O is at rest.)
+                // the first finite score sets it.  (S of this tile is behind the products of the last: O is at
+                // rest.)
                 auto move = [&](float mx, bool up) {
                     const float m_next = up ? mx : m_ref;
-                    const float by = up ? fast_exp2(m_ref - m_next) : 1.f;
+                    const float by = up && m_set ? fast_exp2(m_ref - m_next) : 1.f;
                     m_ref = m_next;
+                    m_set = m_set || up;
                     if (j == 0)
                         return;
                     l_run *= by;
@@ -573,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tmem_st_nowait<16>(t_o + c * 16, ow);
                     }
                 };
-                // (a row without a finite score keeps its reference; NaN scores stay NaN)
+                // (a row without a finite score waits for one; NaN scores stay NaN)
                 auto must_move = [&](float mx) -> bool {
-                    return mx > -CUDART_INF_F && (j == 0 || mx > m_ref + kRescaleThreshold);
+                    return mx > -CUDART_INF_F && (!m_set || mx > m_ref + kRescaleThreshold);
                 };
                 if (j < ns - 1) {
                     float v[4][32];

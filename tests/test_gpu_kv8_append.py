@@ -176,6 +176,64 @@ def test_bad_slots_counters_and_graph(dev):
     assert rlt.rlt_get_device_error() == 0
 
 
+def test_negative_positions_and_other_bases(dev):
+    """Positions of any sign, a base below one: the angle is reduced in whole turns either way."""
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    for base in (10000.0, 0.5, 1.0, 500000.0):
+        q = torch.randn(9, 2, 64, device=dev).bfloat16()
+        k = torch.zeros(9, 1, 64, device=dev).bfloat16()
+        pos = torch.tensor([-1, -77, -100000, 0, 1, 5, 63, -4096, 131071], device=dev)
+        pool = rlt.KV8Pool.empty(1, 1, 1, 16, 64, dev)
+        out = rlt.rlt_kv8_append_rope(pool, 0, k, k, pos, torch.arange(9, device=dev), 64, base, q=q)
+        torch.cuda.synchronize()
+        ref = R.rotate(f64(q), pos.cpu().numpy(), 64, base)
+        norm = np.sqrt((f64(q) ** 2).sum(-1, keepdims=True))
+        # a base below one: frequencies up to 2, angles up to 2^18 radians, off by 2^-53 of themselves on both sides
+        assert np.all(np.abs(f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -22 * norm)
+
+
+def test_binding_refusals(dev):
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    pool = make_pool(rlt, torch, dev, 1, 2, 2, 16, 64, 1)
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev)
+    i = torch.zeros(3, dtype=torch.int64, device=dev)
+    call = lambda **kw: rlt.rlt_kv8_append_rope(**{**dict(pool=pool, bank=0, k_new=k, v_new=k.clone(), positions=i,   # noqa: E731
+                                                          out_loc=i - 1, rot_dim=64, rope_base=BASE), **kw})
+    call()
+    for err, kw in ((TypeError, dict(k_new=k.cpu())), (TypeError, dict(k_new=k.float())), (ValueError, dict(k_new=k[:2])),
+                    (ValueError, dict(v_new=k.transpose(0, 1).contiguous().transpose(0, 1))), (TypeError, dict(positions=i.int())),
+                    (ValueError, dict(q_out=k)), (ValueError, dict(q=k[0])), (ValueError, dict(k_out=k[:2])),
+                    (ValueError, dict(written=torch.zeros(1, 3, dtype=torch.int32, device=dev))),
+                    (ValueError, dict(k_out=torch.zeros(3, 2, 128, dtype=torch.bfloat16, device=dev)[..., ::2])),
+                    (rlt.RltError, dict(bank=1)), (rlt.RltError, dict(rot_dim=5)),
+                    (rlt.RltError, dict(k_new=torch.zeros(1, 2, 64, dtype=torch.bfloat16, device=dev).expand(3, 2, 64)))):
+        with pytest.raises(err):
+            call(**kw)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=dev)
+    table, lens = torch.zeros(2, 1, dtype=torch.int32, device=dev), torch.zeros(2, dtype=torch.int32, device=dev)
+    dec = lambda **kw: rlt.rlt_paged_decode_attn_kv8(**{**dict(pool=pool, bank=0, q=q, page_table=table, seq_lens=lens,  # noqa: E731
+                                                               max_seq_len=16), **kw})
+    assert (dec() == 0).all()
+    for err, kw in ((TypeError, dict(q=q.cpu())), (TypeError, dict(q=q.half())), (ValueError, dict(q=q[..., :32])),
+                    (ValueError, dict(page_table=table[0])), (ValueError, dict(seq_lens=lens[:1])),
+                    (ValueError, dict(out=q[:1])), (TypeError, dict(page_table=table.long())),
+                    (ValueError, dict(q=q.transpose(0, 1).contiguous().transpose(0, 1))),
+                    (rlt.RltError, dict(max_seq_len=5000, split_tokens=16, workspace=torch.empty(16, dtype=torch.uint8, device=dev)))):
+        with pytest.raises(err):
+            dec(**kw)
+    plan = rlt.rlt_plan_prefill([3], 1)
+    pre = lambda **kw: rlt.rlt_prefill_attn(**{**dict(q=k, k=k.clone(), v=k.clone(), plan=plan), **kw})   # noqa: E731
+    pre()
+    for err, kw in ((TypeError, dict(q=k.cpu())), (TypeError, dict(v=k.float())), (ValueError, dict(k=k[:2])),
+                    (ValueError, dict(plan=rlt.rlt_plan_prefill([4], 1))), (ValueError, dict(plan=rlt.rlt_plan_prefill([3], 2))),
+                    (ValueError, dict(out=k[:2])), (ValueError, dict(lse_out=torch.zeros(3, 4, device=dev))),
+                    (rlt.RltError, dict(out=k))):
+        with pytest.raises(err):
+            pre(**kw)
+
+
 def test_no_tokens(dev):
     import torch
     import paged_kv_looped_gb300 as rlt

@@ -90,6 +90,26 @@ def test_rising_scores(dev):
     check(out, lse, q, k, v, [1000], 1.0)
 
 
+def test_first_keys_of_score_minus_infinity(dev):
+    """Scores of -inf (an infinite key component) weigh nothing, also where a row's first tiles hold nothing else."""
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    q, k, v = rows(torch, dev, 400, 2, 1, 64, 13, fused=False)
+    q[..., 0] = 1.0
+    k[:200, :, 0] = float("-inf")
+    k[200:, :, 0] = -3000.0                                     # finite, and far below anything's first guess
+    lse = torch.empty(400, 2, device=dev)
+    out = rlt.rlt_prefill_attn(q, k, v, rlt.rlt_plan_prefill([400], 2), lse_out=lse)
+    torch.cuda.synchronize()
+    assert torch.isneginf(lse[:200]).all()
+    # rows 200..: as if the first 200 keys were not there
+    kk, vv = f64(k)[200:], f64(v)[200:]
+    o, l, mag, terms = R.prefill(f64(q)[200:], kk, vv, [200], 1 / 8)
+    assert np.all(np.abs(f64(lse)[200:] - l) <= R.lse_bound(l, terms, 64))
+    assert np.all(np.abs(f64(out)[200:] - o) <= R.attention_bound(o, mag, terms, 2.0 ** -8))
+    assert rlt.rlt_get_device_error() == 0
+
+
 def test_neighbours_and_rows_behind_hold_anything(dev):
     import torch
     import paged_kv_looped_gb300 as rlt

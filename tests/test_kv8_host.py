@@ -65,7 +65,7 @@ def test_bank_out_of_range(lib, bank):
     dict(loc=0), dict(pos=0), dict(q=0), dict(qo=0), dict(hq=0), dict(k=A * 6 + 2), dict(qo=A * 10 + 8), dict(loc=A + 4),
     dict(ks=250), dict(ks=252), dict(vs=128), dict(qs=260), dict(qs=500), dict(wr=A, batch=4), dict(wr=A, req=A, batch=0),
     dict(qo=A * 6), dict(qo=A * 5 + 16), dict(ko=A * 7), dict(ko=A * 12), dict(qo=A * 5, qs=1024), dict(vo=A * 6),
-    dict(rot=0, pos=0, wr=A, req=A, batch=1)])
+    dict(rot=0, pos=0, wr=A, req=A, batch=1), dict(qo=A), dict(ko=A * 2 + 512), dict(vo=A * 3), dict(ko=A * 4 - 16)])
 def test_append_refusals(lib, change):
     assert append(lib, **change) == INVALID
 
