@@ -24,6 +24,12 @@
 // agree, so every shared-memory read is 16 contiguous bytes of a row (8 for V at head_dim 64);
 // tiles land swizzled by the tensor copy (16-byte chunks XORed by row), and the token order below
 // makes the reads of both K and V free of bank conflicts at head_dim 128.
+//
+// Measured: 64 requests x 16 kv heads x 512-4096 tokens (599 MB) 100 us, 256 log-normal requests x 8 (1.84 GB)
+// 280 us, 8 x 32k-131k tokens x 8 (1.16 GB) 182 us with the join.  While the SMs are busy the cache comes in at
+// 6.65 TB/s (a copy's rate is 6.7); what is left is the grid's start and its last CTAs (10 us).
+// Three CTAs an SM with two stages of two tiles a warp; two CTAs with three such stages took 118 / 318 / 198 us,
+// four stages of one tile 110 / 301 / 190, four CTAs with three stages of one tile 101 / 277 / 181.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -45,7 +51,7 @@ constexpr int kStageTiles = 2;               // 16-token tiles per stage
 constexpr int kStageTokens = kStageTiles * kTileTokens;
 constexpr float kPOffset = 14.f;             // P's largest value is 2^14
 constexpr int kMaxGroup = 8;
-constexpr int kNarrowSplits = 16;            // up to this many splits a warp joins a row alone
+constexpr int kNarrowSplits = 16;            // up to this many splits (two rounds of loads) a warp joins a row alone
 
 template <int D>
 struct Cfg8 {

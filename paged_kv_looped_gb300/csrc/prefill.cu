@@ -10,15 +10,25 @@
 // two heads of one kv head at the same tokens, else one head at 256 consecutive tokens.  It
 // walks the keys in tiles of 128:
 //     S = Q K^T   (128 x 128, K = head_dim)      O += P V   (128 x head_dim, K = 128)
-// on tcgen05 (fp32 accumulators in tensor memory).  4 * 128 * 128 * head_dim flops a tile and key
-// tile take the tensor pipe 1024 clocks at head_dim 128, the softmax of one tile fits beside the
-// products of the other, so the tensor pipe bounds long prompts; short ones are bound by the start of
-// a CTA (first copies, no overlap) and by their ragged last tiles.
+// on tcgen05 (fp32 accumulators in tensor memory: S of both tiles, O of both tiles, 512 columns).
+// 4 * 128 * 128 * head_dim flops a tile and key tile take the tensor pipe 1024 clocks at head_dim 128.
+// A tile's chain (softmax, then P V and the next S, and the hand-overs between them) takes 2600 clocks where
+// two tiles' products alone would take 2048, so the chain bounds long prompts, the tensor pipe 80 %
+// busy: 15973 tokens x 64 heads 2530 us (1650 TFLOP/s, 84 % of a large cuBLAS product's measured rate).
+// Short prompts lose more to each item's first and last key tiles, whose chain is half empty (16 prompts
+// of 1024-2000 tokens x 32 heads: 297 us, 970 TFLOP/s, tensor pipe 52 % busy).
 //
-// Roles: warps 0-3 / 4-7 softmax of tile 0 / 1 (a thread owns one row = one tensor-memory lane:
-// row maxima and sums need no exchange), warp 8 / 9 the MMAs of tile 0 / 1, warp 10 the copies.  P (bf16)
-// is written over the S it came from.  The reference maximum of a row moves only when the running
-// maximum exceeds it by 2^8, so O is rescaled rarely, by the row's own thread.
+// Roles: warps 0-3 / 4-7 softmax of tile 0 / 1 (a thread owns one row = one tensor-memory lane: row maxima and
+// sums need no exchange), warp 8 / 9 the MMAs of tile 0 / 1, warp 10 the works and the copies.  The CTAs are
+// persistent: each takes over blocks the hardware has not started yet (cluster launch control), so
+// that the copies and the first S of the next item run beside the end of the last (8192 tokens x 32
+// heads 351 -> 333 us; 16 prompts of 1024-2000 tokens 407 -> 328).  P (bf16) is written over the S
+// it came from, in two halves that the products take one by one.  The reference maximum of a row moves only when
+// the running maximum exceeds it by 2^8, so O is rescaled rarely, by the row's own thread.
+//
+// Tried and slower or equal at 8192 tokens x 32 heads: polling instead of suspended waits in the MMA threads
+// (351 -> 419 us), no maximum but a limit on the weights' sum (376), one MMA thread for both tiles (350), the
+// output written behind the next item's first softmax (326 -> 349).
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -40,13 +50,15 @@ constexpr int kThreads = 12 * 32;            // warp 11 only fills the third war
 // Registers a thread: 168 at launch (384 threads); the softmax warpgroups take up what the third one
 // gives back: 2 * 208 + 88 = 3 * 168.
 constexpr int kRegsSoftmax = 208, kRegsRest = 88;
-constexpr float kRescaleThreshold = 8.f;     // log2 units
+constexpr float kRescaleThreshold = 8.f;     // log2 units: weights of up to 2^8
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kPartsFrom = 6;                // items of the largest size an SM's share has to hold
 constexpr int64_t kL2Share = 48 << 20;       // of K and V in use at a time (L2 is 126 MB)
 constexpr int kOutBytes = 32 * 128;
 constexpr int kItemFields = 4;               // first row of the sequence, its length, first query of the item, 0
 
+// The output's staging takes the place of a fifth ring slot at head_dim 128: five slots and no staging 326 us, four
+// slots 330, four and the staging 320 (8192 tokens x 32 heads).
 template <int D>
 struct PCfg {
     static constexpr int kStages = D == 128 ? 4 : 8;             // K/V ring slots
@@ -317,11 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp < kLoadWarp && tc::elect_one()) {
             // ---------------------------------------------------------- products
-            // One thread a tile, in the order S | PV S' | PV' S'' ...: MMAs of one thread run in issue order,
-            // so S of the next key tile may overwrite the P that the PV before it reads.  A wait costs a thread
-            // about 75 clocks and a full MMA queue holds it up; with a thread a tile neither delays the other
-            // tile's products.  An MMA keeps the tensor pipe 64 clocks, so its issue has to take less: the
-            // descriptors are the tile's plus constants.
+            // One thread a tile, in the order S | PV S' | PV' S'' ...: MMAs of one thread run in issue order, so S of
+            // the next key tile may overwrite the P that the PV before it reads.  An MMA keeps the tensor pipe 64
+            // clocks, so its issue has to take less: descriptors advance by constants (computed anew for each
+            // MMA, they bounded the kernel: 476 us where these take 376, 8192 tokens x 32 heads).
             const int s = warp - kMmaWarp;
             constexpr uint32_t id_s = tc::instr_desc_bf16(128, 128, false);
             constexpr uint32_t id_o = tc::instr_desc_bf16(128, D, true);
@@ -372,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars[bar]);
             };
             // P V and the S behind it are issued as one: the two threads' MMAs would else alternate, both tiles' S
-            // would come at the same time, and both softmaxes would then want the same units at once.
+            // would come at the same time, and both softmaxes would then want the same units at once (8 ragged
+            // prompts 171 -> 164 us, 8192 tokens x 16 heads of 2 kv heads 200 -> 166).
             volatile int *turn = abort_flag + 1;
             auto take_turn = [&]() -> bool {
                 for (uint32_t it = 1; it != 0; ++it) {
@@ -694,10 +706,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                // The warp's rows, 64 dims at a time, through shared memory and a tensor copy: a lane's row is a line of its
-                // own for every store instruction, and 8 warps' stores of that kind held up the shared-memory pipe (and
-                // with it every barrier of the CTA) for 2300 clocks a tile.  Rows at the end of a sequence are
-                // stored directly: the copy's box would reach into the next one's.
+                // The warp's rows, 64 dims at a time, through shared memory and a tensor copy: a lane's row is a line
+                // of its own for every store instruction, and 8 warps' stores of that kind held up the shared-
+                // memory pipe (and with it every barrier of the CTA) for 2300 clocks a tile.  Rows at the end
+                // of a sequence are stored directly: the copy's box would reach into the next one's.
                 if (q_tok - lane + 31 < wk.len) {
                     unsigned char *mine = base + C::kOutOff + warp * kOutBytes;
 #pragma unroll
