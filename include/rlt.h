@@ -17,8 +17,8 @@
  * (rlt_get_device_error).
  *
  * Debug mode: with RLT_VALIDATE=1 in the environment (read at each call),
- * rlt_kv_append, rlt_paged_decode_attn and rlt_paged_decode_attn_prefix first
- * synchronise the stream, copy the batch's device arrays to the host and check
+ * rlt_kv_append, rlt_paged_decode_attn, rlt_paged_decode_attn_prefix,
+ * rlt_kv8_append_rope and rlt_paged_decode_attn_kv8 first synchronise the stream, copy the batch's device arrays to the host and check
  * them: append slots inside the pool and distinct; page-table entries in use
  * and lengths in range, and, with a fused append, each request's newest slot
  * on a page no other request maps (rlt_validate_batch's rules).  A violation
@@ -95,13 +95,13 @@ typedef enum rlt_status {
 
 /*
  * Flags of the attention calls (rlt_paged_decode_attn, rlt_paged_decode_attn_prefix,
- * rlt_paged_extend_attn).
+ * rlt_paged_extend_attn, rlt_paged_decode_attn_kv8, rlt_prefill_attn).
  *
  * RLT_ATTN_EARLY_START: the call's first kernels are launched as programmatic
  * dependents of the kernel ahead of them in the stream (Hopper/Blackwell
  * programmatic dependent launch; under stream capture, programmatic graph edges),
  * so they may be scheduled while that kernel still runs -- as soon as it lets its
- * dependents start, which every kernel of this library does at its start.  Before
+ * dependents start, which every attention kernel of this library does at its start.  Before
  * the work ahead of them has completed they only read the page table, the lengths,
  * the shared-prefix plan and the cached K/V rows of `bank`, and issue the copies of
  * those rows; they read q, k_new and v_new, and write out, lse_out, the workspace

@@ -207,15 +207,23 @@ rlt_status current_device_info(unsigned int **err, int *num_sms) { return device
 
 rlt_status validate_slots(const int64_t *out_loc, int32_t n_tokens, int64_t num_slots, cudaStream_t stream)
 {
-    return validate_enabled() ? check_slots(out_loc, n_tokens, num_slots, stream) : RLT_OK;
+    try {
+        return validate_enabled() ? check_slots(out_loc, n_tokens, num_slots, stream) : RLT_OK;
+    } catch (...) {
+        return RLT_ERR_INVALID_ARG;              // no host memory for the copies
+    }
 }
 
 rlt_status validate_lengths(const int32_t *page_table, int32_t max_pages, const int32_t *seq_lens, int32_t batch,
                             int64_t num_pages, int32_t page_size, cudaStream_t stream)
 {
-    return validate_enabled() ? validate_attention_batch(page_table, max_pages, seq_lens, batch, num_pages, page_size,
-                                                         false, stream)
-                              : RLT_OK;
+    try {
+        return validate_enabled() ? validate_attention_batch(page_table, max_pages, seq_lens, batch, num_pages, page_size,
+                                                             false, stream)
+                                  : RLT_OK;
+    } catch (...) {
+        return RLT_ERR_INVALID_ARG;              // no host memory for the copies
+    }
 }
 
 rlt_status check_decode_args(const rlt_kv_pool *pool, int32_t bank, const void *q, const void *k_new,

@@ -28,7 +28,9 @@
 //
 // Tried and slower or equal at 8192 tokens x 32 heads: polling instead of suspended waits in the MMA threads
 // (351 -> 419 us), no maximum but a limit on the weights' sum (376), one MMA thread for both tiles (350), the
-// output written behind the next item's first softmax (326 -> 349).
+// output written behind the next item's first softmax (326 -> 349), four further warps for the output (320 -> 335:
+// the softmax warps then have 176 registers instead of 208), two threads a row (411: the units bound the
+// softmax, not one thread's latency).
 #include <cuda.h>
 #include <math_constants.h>
 
