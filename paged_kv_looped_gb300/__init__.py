@@ -626,7 +626,7 @@ class KV8Pool:
         nb, P, Hkv, ps, D = k.shape
         self.num_banks, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = nb, P, Hkv, ps, D
         self.struct = rlt_kv8_pool(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), P, nb, Hkv, ps, D)
-        self.ref = ctypes.byref(self.struct)
+        self.ref, self.address = ctypes.byref(self.struct), ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, num_banks, num_pages, num_kv_heads, page_size, head_dim, device="cuda"):
@@ -635,6 +635,25 @@ class KV8Pool:
         shape = (num_banks, num_pages, num_kv_heads, page_size, head_dim)
         return cls(*(torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
                    *(torch.empty(shape[:4], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+_bound = None
+
+
+def _plain():
+    """The C marshaller of calls in their plain form (csrc/marshal.c): its functions return the library's status, or
+    None for any other call, which the Python code behind them checks and makes."""
+    global _bound
+    if _bound is None:
+        import torch
+
+        from . import _marshal as m
+        at = lambda name: ctypes.cast(getattr(load(), name), ctypes.c_void_p).value      # noqa: E731
+        m.bind(torch.Tensor, torch.bfloat16, torch.int32, torch.int64, torch.float32, torch._C._cuda_getDevice,
+               torch._C._cuda_getCurrentRawStream, at("rlt_kv8_append_rope"), at("rlt_paged_decode_attn_kv8"),
+               at("rlt_prefill_attn"))
+        _bound = m
+    return _bound
 
 
 def _device_index():
@@ -713,6 +732,12 @@ def rlt_kv8_append_rope(pool: KV8Pool, bank: int, k_new, v_new, positions, out_l
     (views of one projection allowed), positions and out_loc int64 [N] (negative slot = nothing is written for
     the entry).  q_out: the rotated queries (made if q is given without it: zeros where an entry is skipped);
     k_out / v_out (optional): bf16 [N][Hkv][D], the rows as the pool holds them.  Returns q_out (None without q)."""
+    if written is None and request is None:
+        st = (_bound or _plain()).append(pool.address, pool.device_index, pool.num_kv_heads, pool.head_dim, bank, k_new,
+                                           v_new, positions, out_loc, rot_dim, rope_base, q, q_out, k_out, v_out, stream)
+        if st is not None:
+            _check(st, "rlt_kv8_append_rope")
+            return q_out
     import torch
     bf16, i64, dev = torch.bfloat16, torch.int64, _device_index()
     n, Hkv, D = out_loc.numel(), pool.num_kv_heads, pool.head_dim
@@ -757,6 +782,12 @@ def rlt_paged_decode_attn_kv8(pool: KV8Pool, bank: int, q, page_table, seq_lens,
                               lse_out=None, workspace=None, scale: float = 0.0, split_tokens: int = 0, stream=None,
                               early_start: bool = False):
     """Paged decode attention over one bank of an 8-bit pool; arguments as rlt_paged_decode_attn."""
+    st = (_bound or _plain()).decode(pool.address, pool.device_index, pool.head_dim, bank, q, page_table, seq_lens,
+                                       max_seq_len, out, lse_out, workspace, scale, split_tokens,
+                                       ATTN_EARLY_START if early_start else 0, stream)
+    if st is not None:
+        _check(st, "rlt_paged_decode_attn_kv8")
+        return out
     import torch
     bf16, i32, dev = torch.bfloat16, torch.int32, _device_index()
     if q.dim() != 3 or q.shape[2] != pool.head_dim:
@@ -823,6 +854,12 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
     """Causal attention over packed prompts: q bf16 [N][Hq][D], k/v bf16 [N][Hkv][D] (views of one projection
     allowed), N >= the plan's rows; rows behind the last sequence are left alone (zeros in an out made here).
     Returns out [N][Hq][D]."""
+    st = (_bound or _plain()).prefill(q, k, v, plan.dev, plan.num_items, plan.num_rows, plan.max_key_tiles,
+                                        plan.total_key_tiles, plan.query_group, out, lse_out, scale,
+                                        ATTN_EARLY_START if early_start else 0, stream)
+    if st is not None:
+        _check(st, "rlt_prefill_attn")
+        return out
     import torch
     bf16, dev = torch.bfloat16, _device_index()
     if q.dim() != 3 or k.dim() != 3:

@@ -1,4 +1,5 @@
-"""Build librlt.so (sm_103a) in-tree with nvcc: one object per .cu, compiled in parallel."""
+"""Build librlt.so (sm_103a) in-tree with nvcc, one object per .cu, compiled in parallel, and the binding's
+argument marshaller (_marshal.so, C) with the host compiler."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -6,6 +7,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librlt.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -28,14 +31,14 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".c"))]
     return files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -57,6 +60,13 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE,
+                        "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling marshal.c failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources())) as ex:
         results = list(ex.map(compile_one, sources()))
     if verbose_ptxas:
