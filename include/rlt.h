@@ -101,7 +101,9 @@ typedef enum rlt_status {
  * dependents of the kernel ahead of them in the stream (Hopper/Blackwell
  * programmatic dependent launch; under stream capture, programmatic graph edges),
  * so they may be scheduled while that kernel still runs -- as soon as it lets its
- * dependents start, which every attention kernel of this library does at its start.  Before
+ * dependents start, which every attention kernel of this library and
+ * rlt_kv8_append_rope's do at their start (those of the 8-bit cache's and the prompts' calls
+ * without the flag once the work ahead of them has completed).  Before
  * the work ahead of them has completed they only read the page table, the lengths,
  * the shared-prefix plan and the cached K/V rows of `bank`, and issue the copies of
  * those rows; they read q, k_new and v_new, and write out, lse_out, the workspace
@@ -113,7 +115,9 @@ typedef enum rlt_status {
  * attention) write only q, k_new, v_new.  Not with a separate rlt_kv_append into
  * the same bank right before the call.  Without the flag the first kernels start
  * after all earlier work in the stream; inside a call the combine always starts
- * behind the partial kernels this way (it is this library's own kernel).
+ * behind the partial kernels this way (it is this library's own kernel).  The calls of
+ * the 8-bit cache and of prompts are launched this way without the flag too, but read and
+ * write nothing until the kernel ahead of them has completed.
  */
 #define RLT_ATTN_EARLY_START 1u
 
@@ -569,7 +573,8 @@ RLT_API size_t rlt_paged_decode_kv8_workspace_size(int32_t batch, int32_t num_q_
  * K_j and V_j the values the pool stands for.  Arguments, workspace, flags, the clamping
  * of lengths and the skipping of bad pages as there, without the fused append (the
  * new token's rows are appended first, by rlt_kv8_append_rope; so RLT_ATTN_EARLY_START
- * only where that append is not among the kernels that may still run).  Supported:
+ * only where that append is not among the kernels that may still run: not right behind
+ * it).  Supported:
  * head_dim 64 or 128; any num_q_heads/num_kv_heads from 1 to 8.  Scores and sums
  * are fp32; a query enters with its bf16 bits down to 2^-38 of its head's largest
  * magnitude, a weight with 11 bits down to 2^-28 of the largest weight x value scale.

@@ -116,6 +116,8 @@ template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_chunks_kernel(const Kv8AppendParams p, int splits)
 {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    pdl_wait();                                  // (launched while the kernel ahead ends)
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int64_t i = w / splits;
@@ -257,6 +259,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(con
 {
     constexpr int kWords = D / 64;               // 32-bit words of a row that a lane loads
     __shared__ __align__(16) float rows[kAppendWarps][kBatch][D];
+    pdl_wait();                                  // (launched while the kernel ahead ends)
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int64_t i = w / splits;
@@ -374,11 +378,8 @@ cudaError_t launch_append_typed(const Kv8AppendParams &p, cudaStream_t stream)
     const int64_t want = kSpreadWarps / (p.n_tokens > 0 ? p.n_tokens : 1);
     const int splits = (int)(want < 1 ? 1 : want < rounds ? want : rounds);
     const int64_t blocks = ((int64_t)p.n_tokens * splits + kAppendWarps - 1) / kAppendWarps;
-    if (chunks)
-        kv8_append_chunks_kernel<D><<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(p, splits);
-    else
-        kv8_append_pairs_kernel<D><<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(p, splits);
-    return cudaGetLastError();
+    return launch_kernel(chunks ? kv8_append_chunks_kernel<D> : kv8_append_pairs_kernel<D>, dim3((unsigned)blocks),
+                         dim3(kAppendWarps * 32), 0, stream, true, p, splits);
 }
 
 }  // namespace

@@ -117,7 +117,7 @@ __device__ __forceinline__ int chunk_offset(int r, int c)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 3)
     kv8_partial_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const DecodeParams p, const uint8_t *__restrict__ k_exp, const uint8_t *__restrict__ v_exp)
+                       const DecodeParams p, const uint8_t *__restrict__ k_exp, const uint8_t *__restrict__ v_exp, int early)
 {
     using C = Cfg8<D>;
     constexpr int kHalves = D / 64;              // 64-dim halves of a K row
@@ -125,6 +125,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // The grid starts while the kernel ahead ends.  Without the early start nothing is read before it has, and
+    // the kernel behind starts no earlier either.
+    if (early == 0)
+        pdl_wait();
     pdl_launch_dependents();
     const int split = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -548,7 +552,7 @@ cudaError_t launch_typed8(const DecodeParams &p, const Kv8Bank &bank, cudaStream
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
     e = launch_kernel(kv8_partial_kernel<D>, dim3(p.max_splits, p.num_kv_heads, p.batch), dim3(kThreads),
-                      C::kSmemBytes, stream, early, kmap, vmap, p, bank.k_exp, bank.v_exp);
+                      C::kSmemBytes, stream, true, kmap, vmap, p, bank.k_exp, bank.v_exp, early ? 1 : 0);
     if (e != cudaSuccess || p.max_splits <= 1)
         return e;
     const int64_t q_rows = (int64_t)p.batch * p.num_q_heads;

@@ -182,7 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(base + C::kFlagOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + C::kFlagOff + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_launch_dependents();
+    // The CTA is set up while the kernel ahead ends. Without the early start nothing is read before it has, and
+    // the kernel behind starts no earlier either.
+    if (p.early != 0)
+        pdl_launch_dependents();
 
     const int G = p.num_q_heads / p.num_kv_heads;
     const bool pair = G % 2 == 0;                // tile 1: the next head, else the next 128 tokens
@@ -206,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::prefetch_tmap(&vmap);
             tc::prefetch_tmap(&omap);
         }
-        first_work = find(blockIdx.x);
+        if (p.early != 0)
+            first_work = find(blockIdx.x);
     }
     if (tid < C::kNumBars) {
         const int i = tid;
@@ -252,6 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // for while this one's copies are issued.  Ring order K0, V0, K1, V1, ...; rows behind
             // the last one of the array read as zeros.
             pdl_wait();
+            if (p.early == 0) {
+                pdl_launch_dependents();
+                first_work = find(blockIdx.x);
+            }
             auto load = [&](unsigned char *dst, const CUtensorMap *map, int head, int row, uint64_t *bar) {
                 mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
@@ -818,8 +826,9 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
         kv_heads = p.num_kv_heads;
     PrefillParams c = p;
     c.chunk_units = (int32_t)kv_heads * per_kv;
+    c.early = early ? 1 : 0;
     return launch_kernel(prefill_kernel<D>, dim3(p.num_items * per_kv * p.num_kv_heads), dim3(kThreads), C::kSmem,
-                         stream, early, qmap, kmap, vmap, omap, c);
+                         stream, true, qmap, kmap, vmap, omap, c);
 }
 
 }  // namespace

@@ -238,6 +238,7 @@ struct PrefillParams {
     int32_t max_tiles, total_tiles;   // key tiles of the plan's largest item and of all items
     int32_t num_sms;
     int32_t chunk_units;         // units of heads that run through the items together (launch_prefill sets it)
+    int32_t early;               // items may be read before the kernels ahead have completed (launch_prefill sets it)
     float qscale;                // softmax scale * log2(e)
 };
 
