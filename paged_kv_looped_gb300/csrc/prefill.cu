@@ -14,9 +14,9 @@
 // 4 * 128 * 128 * head_dim flops a tile and key tile take the tensor pipe 1024 clocks at head_dim 128.
 // A tile's chain (softmax, then P V and the next S, and the hand-overs between them) takes 2600 clocks where
 // two tiles' products alone would take 2048, so the chain bounds long prompts, the tensor pipe 80 %
-// busy: 15973 tokens x 64 heads 2530 us (1650 TFLOP/s, 84 % of a large cuBLAS product's measured rate).
+// busy: 15973 tokens x 64 heads 2514 us (1660 TFLOP/s, 84 % of a large cuBLAS product's measured rate).
 // Short prompts lose more to each item's first and last key tiles, whose chain is half empty (16 prompts
-// of 1024-2000 tokens x 32 heads: 297 us, 970 TFLOP/s, tensor pipe 52 % busy).
+// of 1024-2000 tokens x 32 heads: 295 us, 980 TFLOP/s, tensor pipe 52 % busy).
 //
 // Roles: warps 0-3 / 4-7 softmax of tile 0 / 1 (a thread owns one row = one tensor-memory lane: row maxima and
 // sums need no exchange), warp 8 / 9 the MMAs of tile 0 / 1, warp 10 the works and the copies.  The CTAs are
