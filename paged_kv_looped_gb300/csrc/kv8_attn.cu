@@ -28,8 +28,9 @@
 // Measured: 64 requests x 16 kv heads x 512-4096 tokens (599 MB) 97 us, 256 log-normal requests x 8 (1.84 GB)
 // 275 us, 8 x 32k-131k tokens x 8 (1.16 GB) 178 us with the join.  While the SMs are busy the cache comes in at
 // 6.65 TB/s (a copy's rate is 6.7); what is left is the grid's start and its last CTAs (7 us).
-// Launched behind the end of the kernel ahead (100 / 280 / 182 us): three CTAs an SM with two stages of two tiles a warp; two CTAs with three such stages took 118 / 318 / 198,
-// four stages of one tile 110 / 301 / 190, four CTAs with three stages of one tile 101 / 277 / 181.
+// Three CTAs an SM with two stages of two tiles a warp; calls in a row, launched only at the end of the kernel
+// ahead, took 100 / 275 / 178 us with them, 118 / 318 / 198 with two CTAs of three such stages, 110 / 301 / 190
+// with four stages of one tile, 101 / 277 / 181 with four CTAs of three stages of one tile.
 #include <cuda.h>
 #include <math_constants.h>
 
