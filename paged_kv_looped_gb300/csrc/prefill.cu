@@ -228,8 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid < 16)
         reinterpret_cast<uint32_t *>(base + C::kBadOff)[tid] = 0u;
-    if (warp == kMmaWarp)
+    if (warp == kMmaWarp) {
+        pdl_wait();                              // the kernel ahead may still have tensor memory to allocate
         tc::tmem_alloc(tslot, kTmemCols);
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
