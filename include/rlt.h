@@ -577,7 +577,8 @@ RLT_API size_t rlt_paged_decode_kv8_workspace_size(int32_t batch, int32_t num_q_
  * it).  Supported:
  * head_dim 64 or 128; any num_q_heads/num_kv_heads from 1 to 8.  Scores and sums
  * are fp32; a query enters with its bf16 bits down to 2^-38 of its head's largest
- * magnitude, a weight with 11 bits down to 2^-28 of the largest weight x value scale.
+ * magnitude, a weight with 11 bits down to 2^-28 of the largest weight x value scale
+ * (a row of zero values takes no part in that largest until it outweighs the others by 2^100).
  * Rows of the pool behind a request's end are not looked at, whatever they hold.
  */
 RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t bank, const void *q,

@@ -6,7 +6,8 @@
 // held e4m3 numbers and everything in log2 units
 //     s_j = qscale <q, k8_j> 2^(ke_j),     out = sum_j 2^(s_j) 2^(ve_j) v8_j / sum_j 2^(s_j).
 // The value's scale rides in the exponent: w_j = s_j + ve_j, and P_j = 2^(w_j - m + 14) against a
-// running maximum m of w multiplies v8_j.
+// running maximum m of w multiplies v8_j.  A row of zero values carries the scale 2^0 whatever its neighbours'
+// scales are; it would raise m and cost the others' weights their bits, so it counts with 2^-100.
 //
 // What bounds it: the cache's bytes, 2 (D + 1) per token and kv head; 4 G flop for each pair of
 // them.  At 6.7 TB/s an SM takes in about 21 bytes a clock, and a CUDA-core kernel would have to
@@ -51,6 +52,7 @@ constexpr int kStages = 2;                   // copy ring depth per warp
 constexpr int kStageTiles = 2;               // 16-token tiles per stage
 constexpr int kStageTokens = kStageTiles * kTileTokens;
 constexpr float kPOffset = 14.f;             // P's largest value is 2^14
+constexpr float kZeroRowExp = -100.f;        // of a row of zero values: l stays below 2^(100 + 21) of 2^m
 constexpr int kMaxGroup = 8;
 constexpr int kNarrowSplits = 16;            // up to this many splits (two rounds of loads) a warp joins a row alone
 
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         int valid[kStageTiles];                  // tokens of each tile (warp-uniform)
         float sv[kStageTiles][4], wv[kStageTiles][4];
         float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+        bool one = false;                        // a value scale of 2^0 among this lane's tokens
 #pragma unroll
         for (int u = 0; u < kStageTiles; ++u) {
             valid[u] = ((have >> (kStageTiles * i + u)) & 1u) ? min(kTileTokens, L - tok0 - u * kTileTokens) : 0;
@@ -284,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             const float va = (float)((int)es[kStageTokens + u * kTileTokens + tok_g] - kExpBias);
             const float vb = (float)((int)es[kStageTokens + u * kTileTokens + tok_g + 8] - kExpBias);
             const bool in_a = tok_g < valid[u], in_b = tok_g + 8 < valid[u];
+            one |= va == 0.f || vb == 0.f;
             sv[u][0] = in_a ? c[0] * sc0 * ka : -CUDART_INF_F;
             sv[u][1] = in_a ? c[1] * sc1 * ka : -CUDART_INF_F;
             sv[u][2] = in_b ? c[2] * sc0 * kb : -CUDART_INF_F;
@@ -298,9 +302,46 @@ __global__ void __launch_bounds__(kThreads, 3)
         x0 = fmaxf(m0, warp_max_xor(x0, 4));
         x1 = fmaxf(m1, warp_max_xor(x1, 4));
         if (__any_sync(kFullMask, x0 != m0 || x1 != m1)) {
-            const float a0 = x0 == m0 ? 1.f : fast_exp2(m0 - x0), a1 = x1 == m1 ? 1.f : fast_exp2(m1 - x1);
-            l0 *= a0;
-            l1 *= a1;
+            // The maximum rises, but not for a row of zeros.  (Where it does not rise they do no harm.)
+            if (__any_sync(kFullMask, one)) {
+                x0 = x1 = -CUDART_INF_F;
+#pragma unroll
+                for (int u = 0; u < kStageTiles; ++u) {
+                    // Scale 2^0: zeros, or (rarely) values of 128 to 256.  The four lanes of a token look at a quarter
+                    // of its row each; negative zeros count too.
+                    const uint8_t *ve = es + kStageTokens + u * kTileTokens;
+                    uint32_t ra = 0u, rb = 0u;
+#pragma unroll
+                    for (int hh = 0; hh < kHalves; ++hh) {
+                        const unsigned char *vt = vs + u * C::kTileBytes;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + chunk_offset<D>(tok_g, t + 4 * hh));
+                        const uint4 y = *reinterpret_cast<const uint4 *>(vt + chunk_offset<D>(tok_g + 8, t + 4 * hh));
+                        ra |= x.x | x.y | x.z | x.w;
+                        rb |= y.x | y.y | y.z | y.w;
+                    }
+                    ra |= __shfl_xor_sync(kFullMask, ra, 1);
+                    ra |= __shfl_xor_sync(kFullMask, ra, 2);
+                    rb |= __shfl_xor_sync(kFullMask, rb, 1);
+                    rb |= __shfl_xor_sync(kFullMask, rb, 2);
+                    if (ve[tok_g] == kExpBias && (ra & 0x7f7f7f7fu) == 0u) {
+                        wv[u][0] = sv[u][0] + kZeroRowExp;
+                        wv[u][1] = sv[u][1] + kZeroRowExp;
+                    }
+                    if (ve[tok_g + 8] == kExpBias && (rb & 0x7f7f7f7fu) == 0u) {
+                        wv[u][2] = sv[u][2] + kZeroRowExp;
+                        wv[u][3] = sv[u][3] + kZeroRowExp;
+                    }
+                    x0 = fmaxf(x0, fmaxf(wv[u][0], wv[u][2]));
+                    x1 = fmaxf(x1, fmaxf(wv[u][1], wv[u][3]));
+                }
+                x0 = fmaxf(m0, warp_max_xor(x0, 4));
+                x1 = fmaxf(m1, warp_max_xor(x1, 4));
+            }
+            // 2^(m - x) in two halves: it may be below fp32's smallest where l (up to 2^121) times it is not
+            const float h0 = x0 == m0 ? 1.f : fast_exp2(0.5f * (m0 - x0)), h1 = x1 == m1 ? 1.f : fast_exp2(0.5f * (m1 - x1));
+            const float a0 = h0 * h0, a1 = h1 * h1;
+            l0 = l0 * h0 * h0;
+            l1 = l1 * h1 * h1;
 #pragma unroll
             for (int d = 0; d < kDimTiles; ++d) {
                 acc[d][0] *= a0;
@@ -407,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float *row = mg + (w * kMaxGroup + h) * C::kMergeStride;
-            const float sc = exp2f(row[D] - M);
-            ls = fmaf(row[D + 1], sc, ls);
+            const float half = exp2f(0.5f * (row[D] - M)), sc = half * half;   // (as the running rescale)
+            ls = fmaf(row[D + 1] * half, half, ls);
             o0 = fmaf(row[d0 + 0], sc, o0);
             o1 = fmaf(row[d0 + 1], sc, o1);
             o2 = fmaf(row[d0 + 2], sc, o2);
