@@ -552,7 +552,8 @@ typedef struct rlt_kv8_pool {
  *                    The angle is reduced modulo a turn in 64-bit fixed point; sin, cos
  *                    and the rotation are fp32: off by about 2^-23 of the pair's norm
  *                    before the one rounding to bf16 or e4m3
- *   request, written, batch  as rlt_kv_append_rope
+ *   request, written, batch  as rlt_kv_append_rope; a position below 0 counts nothing, one past
+ *                    2^31 - 2 counts as that
  * An output may be the call's own input of the same kind (same address, rows
  * num_heads*head_dim apart); any other overlap, also with the pool, is RLT_ERR_INVALID_ARG.  All arrays but
  * positions, out_loc, request and written (their elements' alignment) 16-byte aligned.

@@ -76,11 +76,12 @@ __device__ __forceinline__ int64_t token_slot(const Kv8AppendParams &p, int64_t 
     return -1;
 }
 
+// The request's counter becomes at least the position + 1, as an int32 holds it; a position below 0 counts nothing.
 __device__ __forceinline__ void count_written(const Kv8AppendParams &p, int64_t i)
 {
     const int32_t r = p.request[i];
     if (r >= 0 && r < p.batch)
-        atomicMax(&p.written[r], (int32_t)min(p.positions[i] + 1, (int64_t)INT32_MAX));
+        atomicMax(&p.written[r], (int32_t)min(max(p.positions[i], (int64_t)-1), (int64_t)INT32_MAX - 1) + 1);
     else
         record_error(p.err, RLT_DEVERR_BAD_SLOT);
 }
