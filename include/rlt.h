@@ -549,7 +549,8 @@ typedef struct rlt_kv8_pool {
  *   positions        int64 [n_tokens], any value; may be NULL with rot_dim == 0
  *   rot_dim          even, 0 (no rotation) .. head_dim; pairs (i, i + rot_dim/2) turn by
  *                    positions[i] * rope_base^(-2i/rot_dim), as rlt_kv_append_rope.
- *                    The angle is reduced modulo a turn in 64-bit fixed point; sin, cos
+ *                    The angle is reduced modulo a turn in 64-bit fixed point (off by
+ *                    |positions[i]| * 2^-60 radians for bases from 100, 2^-56 from 1); sin, cos
  *                    and the rotation are fp32: off by about 2^-23 of the pair's norm
  *                    before the one rounding to bf16 or e4m3
  *   request, written, batch  as rlt_kv_append_rope; a position below 0 counts nothing, one past

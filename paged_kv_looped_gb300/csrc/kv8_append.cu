@@ -7,8 +7,8 @@
 //
 // The angle of pair i at position p is p * base^(-2i/rot) radians.  Its turns, p * base^(-2i/rot)
 // / 2 pi, matter modulo 1 only: with the frequency as a 64-bit fixed-point fraction F_i of a turn,
-// the low 64 bits of p * F_i are that fraction of a turn, exactly reduced for any position (F_i
-// carries fp64's rounding, 2^-53 relative: 2^-36 turns at position 2^17).  The nearest quarter
+// the low 64 bits of p * F_i are that fraction of a turn, exactly reduced for any position (F_i is made
+// in extended precision: at position 2^31 the angle is off by 2^-29 rad).  The nearest quarter
 // turn goes to the quadrant, the rest, at most pi/4, to the Taylor polynomials of sin and cos.
 #include <cmath>
 
@@ -386,13 +386,16 @@ cudaError_t launch_append_typed(const Kv8AppendParams &p, cudaStream_t stream)
 
 }  // namespace
 
-// F_i = base^(-2i/rot) / 2 pi turns per position, modulo one turn, as a 64-bit fraction.
+// F_i = base^(-2i/rot) / 2 pi turns per position, modulo one turn, as a 64-bit fraction.  Positions multiply its
+// error, so it needs all 64 bits: long double (a mantissa of 64 bits or more), one power and a product a pair.
 void rope_frequencies(int rot_dim, double base, uint64_t *freq)
 {
-    for (int i = 0; i < rot_dim / 2; ++i) {
-        const double turns = std::fmod(std::pow(base, -2.0 * i / rot_dim) * 0.15915494309189535, 1.0);
-        freq[i] = (uint64_t)(turns * 18446744073709551616.0);
-    }
+    if (rot_dim < 2)
+        return;
+    const long double step = std::pow((long double)base, -2.0L / rot_dim);
+    long double turns = 0.1591549430918953357688837633725143620L;
+    for (int i = 0; i < rot_dim / 2; ++i, turns *= step)
+        freq[i] = (uint64_t)(std::fmod(turns, 1.0L) * 18446744073709551616.0L);
 }
 
 cudaError_t launch_kv8_append(const Kv8AppendParams &p, cudaStream_t stream)
