@@ -618,7 +618,8 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
  * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
  * fp32; weights enter the product with V as bf16, up to 2^8 (values up to 2^119 cannot
  * overflow by it).  An infinity or NaN in q, k or v reaches the rows whose formula it is
- * part of and no other: not earlier rows, not other sequences.
+ * part of and no other: not earlier rows, not other sequences (an infinity whose weight is
+ * below fp32's smallest as an infinity or a NaN, the same one every time).
  */
 RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t batch, int32_t query_group, int32_t *items,
                                     int32_t max_items, int32_t *sizes);

@@ -81,11 +81,12 @@ struct PCfg {
         kWorkFull = kOFree + 2,              // [2] a work descriptor published
         kWorkFree = kWorkFull + 2,           // [2] every role is done with it
         kNext = kWorkFree + 2,               // the scheduler's answer landed
-        kNumBars = kNext + 1
+        kClean = kNext + 1,                  // [2 works][tile] V of the tile's last keys looked at (a pair's tiles: [0])
+        kNumBars = kClean + 4
     };
     static constexpr int kWorkOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;   // two Work
     static constexpr int kNextOff = kWorkOff + 32;               // the scheduler's 16-byte answer
-    static constexpr int kBadOff = kNextOff + 16;                // [2 items][tile][4] rows with non-finite values
+    static constexpr int kBadOff = kNextOff + 16;                // [2 works][softmax warp] rows with non-finite values
     static constexpr int kFlagOff = kBadOff + 64;
     static constexpr int kSmem = kFlagOff + 16 + 1024;
     static_assert(kNumBars <= kThreads, "a thread a barrier at the start");
@@ -221,6 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             count = 4;                           // the tile's softmax warps
         else if (i >= C::kWorkFree && i < C::kNext)
             count = 10;                          // two MMA threads, eight softmax warps
+        else if (i >= C::kClean)
+            count = pair ? 8 : 4;                // the softmax warps that look
         mbar_init(&bars[i], count);
         *abort_flag = 0;
         *(abort_flag + 1) = 0;
@@ -416,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 take(d, w);
                 if (w.len < 0)
                     break;
-                const int ns = key_tiles(w, s), n = max(key_tiles(w, 0), key_tiles(w, 1));
+                const int ns0 = key_tiles(w, 0), ns = key_tiles(w, s), n = max(ns0, key_tiles(w, 1));
+                uint64_t *clean = &bars[C::kClean + (d & 1) * 2];
                 int k_slot = 0, v_slot = 0;
                 if (!(ok = mbar_wait_or_abort(&bars[C::kQFull + s], d & 1u, abort_flag)))
                     break;
@@ -435,6 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = wait_slot(v_slot)) || (j + 1 < n && !(ok = wait_slot(k_slot))))
                         break;
                     if (j < ns) {
+                        // The values of the last keys have been looked at: a pair's tiles share them, and at an odd group
+                        // tile 0's last keys are ordinary ones of tile 1.  (Waited for before the turn is taken.)
+                        if (j == ns0 - 1 && !(ok = mbar_wait_or_abort(&clean[0], (d / 2) & 1u, abort_flag)))
+                            break;
+                        if (!pair && s == 1 && j == ns - 1 &&
+                            !(ok = mbar_wait_or_abort(&clean[1], (d / 2) & 1u, abort_flag)))
+                            break;
                         // the item before has left O
                         if (j == 0 && items > 0 &&
                             !(ok = mbar_wait_or_abort(&bars[C::kOFree + s], (items - 1) & 1u, abort_flag)))
@@ -508,9 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ns = key_tiles(wk, s), n = max(key_tiles(wk, 0), key_tiles(wk, 1));
             const int q_tok = wk.q0 + s * tok_step + quarter * 32 + lane;    // this thread's query, in its sequence
             const int head0 = pair ? 2 * wk.unit : wk.unit;
-            uint32_t *bad = reinterpret_cast<uint32_t *>(base + C::kBadOff) + (d & 1) * 8;
+            volatile uint32_t *bad = reinterpret_cast<volatile uint32_t *>(base + C::kBadOff) + (d & 1) * 8;
             if (ns == 0 && lane == 0)
-                bad[s * 4 + quarter] = 0u;
+                mbar_arrive(&bars[C::kClean + (d & 1) * 2 + (pair ? 0 : s)]);
             float m_ref = 0.f, l_run = 0.f;
             bool m_set = false;
             for (int j = 0; j < ns; ++j, ++tiles) {
@@ -518,43 +529,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // The tile of the row's own keys: weights of masked keys are 0, but 0 times an infinity or NaN
                     // would stay.  Rows of V past the sequence (they may hold anything) become zeros, and so do
                     // single values that are not finite; their rows are noted, and the epilogue adds what
-                    // a query may see of them.  A lane looks at one row, while S is computed.
+                    // a query may see of them.  It is done while S is computed, each row by one warp, and every product
+                    // that reads these values waits for all of them.  A pair's tiles have the same last keys: 16 rows a
+                    // warp, two lanes a row (at head_dim 128 the second starts four chunks on, in other banks); else
+                    // 32 rows of the tile's own, a lane a row.  (One further warp for all of it took 321 us where this
+                    // takes 298, 16 prompts of 1024-2000 tokens x 32 heads.)
                     const int i = copies + 2 * j + 1;
                     if (!(ok = warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag)))
                         break;
                     unsigned char *vt = base + C::kRingOff + i % C::kStages * C::kTileBytes;
-                    const int r = quarter * 32 + lane;
+                    const int r = pair ? warp * 16 + (lane >> 1) : quarter * 32 + lane;
                     const bool inside = r < wk.len - j * kTile;
+                    auto chunk = [&](int half, int c) -> uint4 * {
+                        const int at = D == 128 ? half * C::kBlock + r * 128 + (((c ^ (half << 2) ^ r) & 7) << 4)
+                                                : r * 128 + ((((half << 2) + c) ^ r) & 7) * 16;
+                        return reinterpret_cast<uint4 *>(vt + at);
+                    };
                     uint32_t big = 0u;
+#pragma unroll 1
+                    for (int half = pair ? lane & 1 : 0; half < (pair ? (lane & 1) + 1 : 2); ++half)
 #pragma unroll
-                    for (int c = 0; c < kBlocks * 8; ++c) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(vt + (c >> 3) * C::kBlock + r * 128 +
-                                                                         (((c ^ r) & 7) << 4));
-                        big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                    }
+                        for (int c = 0; c < D / 16; ++c) {
+                            const uint4 x = *chunk(half, c);
+                            big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                         __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                        }
                     const unsigned odd = __ballot_sync(kFullMask, inside && not_finite(big));
                     if (lane == 0)
-                        bad[s * 4 + quarter] = odd;
-                    __threadfence_block();       // the note before the values go
-                    __syncwarp();
+                        bad[warp] = odd;
                     if (!inside || not_finite(big)) {
 #pragma unroll 1
-                        for (int c = 0; c < kBlocks * 8; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(vt + (c >> 3) * C::kBlock + r * 128 +
-                                                                  (((c ^ r) & 7) << 4));
+                        for (int c = 0; c < (pair ? D / 16 : D / 8); ++c) {
+                            uint4 *at = pair ? chunk(lane & 1, c) : chunk(c / (D / 16), c % (D / 16));
                             uint4 x = *at;
-                            auto clean = [&](uint32_t y) -> uint32_t {
+                            auto finite = [&](uint32_t y) -> uint32_t {
                                 if (!inside)
                                     return 0u;
                                 return ((y & 0x7f80u) == 0x7f80u ? 0u : y & 0xffffu) |
                                        ((y & 0x7f800000u) == 0x7f800000u ? 0u : y & 0xffff0000u);
                             };
-                            *at = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+                            *at = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
                         }
-                        fence_proxy_async();     // (generic writes before the product's reads)
+                        fence_proxy_async();     // (generic writes before the products' reads)
                     }
                     __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars[C::kClean + (d & 1) * 2 + (pair ? 0 : s)]);
                 }
                 if (!(ok = warp_wait(&bars[C::kSFull + s], tiles & 1u, abort_flag)))
                     break;
@@ -687,10 +707,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++items;
                 const float inv = 1.f / l_run;
                 const int64_t at = (int64_t)(wk.row0 + q_tok) * p.num_q_heads + head0 + s * head_step;
-                // rows of V with values that are not finite: of both tiles' last keys (cleaned by either)
+                // Rows of V with values that are not finite, of the keys from q0 on: the last ones of a pair, or of tile
+                // 0 (ordinary ones of tile 1) and then of tile 1.  P V has waited for these barriers, so they have
+                // completed; the probes order the notes' reads behind them (waits here took 303 us for 298).
+                const int words = pair || s == 1 ? 8 : 4;
+                mbar_test_wait(&bars[C::kClean + (d & 1) * 2], (d / 2) & 1u);
+                mbar_test_wait(&bars[C::kClean + (d & 1) * 2 + s], (d / 2) & 1u);
                 uint32_t any_bad = 0u;
-                for (int i = 0; i < 8; ++i)
-                    any_bad |= reinterpret_cast<volatile uint32_t *>(bad)[i];
+                for (int i = 0; i < words; ++i)
+                    any_bad |= bad[i];
                 float o[D / 32][32];
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
@@ -704,10 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars[C::kOFree + s]);
                 if (any_bad != 0u) {
 #pragma unroll 1
-                    for (int b = 0; b < 256; ++b) {
-                        const int key = wk.q0 + (b >> 7) * tok_step + (b & 127);
-                        if (((reinterpret_cast<volatile uint32_t *>(bad)[b >> 5] >> (b & 31)) & 1u) == 0u ||
-                            key > q_tok || key >= wk.len)
+                    for (int b = 0; b < words * 32; b += pair ? 2 : 1) {     // (a pair: a row has two bits, for its halves)
+                        const int key = wk.q0 + (pair ? b >> 1 : b);
+                        if (((bad[b >> 5] >> (b & 31)) & (pair ? 3u : 1u)) == 0u || key > q_tok || key >= wk.len)
                             continue;
                         const uint16_t *vr = p.v + (int64_t)(wk.row0 + key) * p.v_stride + (int64_t)(head0 / G) * D;
 #pragma unroll
@@ -764,8 +788,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(&bars[C::kWorkFree + (d & 1)]);
         }
-        if (!ok)
+        if (!ok) {
             *abort_flag = 1;
+            tc::tmem_wait_st();                  // (no store is under way when the tensor memory is given back)
+        }
         if (lane == 0)
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");        // the output has left shared memory
     }
