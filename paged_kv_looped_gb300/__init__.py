@@ -823,11 +823,12 @@ class PrefillPlan:
     def __init__(self, items, sizes, query_group):
         self.items, self.query_group = items, query_group
         self.num_items, self.num_rows, self.max_key_tiles, self.total_key_tiles = (int(x) for x in sizes)
-        self.dev = None
+        self.dev, self.dev_stream = None, None
 
     def to(self, device):
         import torch
         self.dev = torch.from_numpy(self.items).to(device)
+        self.dev_stream = _current_stream_on(self.dev)
         return self
 
 
@@ -845,6 +846,25 @@ def rlt_plan_prefill(seq_lens, query_group: int = 1) -> PrefillPlan:
     return PrefillPlan(items, sizes, int(query_group))
 
 
+def _current_stream_on(t):
+    """Handle of torch's current stream on t's device, whose allocations t's memory goes back to (None off the GPU)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
+
+
+def _hold(stream, dev, made_on, *tensors):
+    """Arrays of a plan, uploaded on stream `made_on`, that a call is about to read on `stream`: where that is another one,
+    the allocator keeps their memory until the call is done, also if the plan dies when the call returns."""
+    import torch
+    raw = _raw_stream(stream, dev)
+    if raw == made_on:
+        return
+    s = torch.cuda.ExternalStream(raw) if stream is None or isinstance(stream, int) else stream
+    for t in tensors:
+        if t.is_cuda:
+            t.record_stream(s)
+
+
 def _np_ptr(a):
     return a.ctypes.data_as(ctypes.c_void_p)
 
@@ -853,7 +873,9 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
                      early_start: bool = False):
     """Causal attention over packed prompts: q bf16 [N][Hq][D], k/v bf16 [N][Hkv][D] (views of one projection
     allowed), N >= the plan's rows; rows behind the last sequence are left alone (zeros in an out made here).
-    Returns out [N][Hq][D]."""
+    A plan not uploaded yet is uploaded here (not under stream capture).  Returns out [N][Hq][D]."""
+    if plan.dev is not None:
+        _hold(stream, _device_index(), plan.dev_stream, plan.dev)
     st = (_bound or _plain()).prefill(q, k, v, plan.dev, plan.num_items, plan.num_rows, plan.max_key_tiles,
                                         plan.total_key_tiles, plan.query_group, out, lse_out, scale,
                                         ATTN_EARLY_START if early_start else 0, stream)
@@ -876,6 +898,7 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
         raise ValueError("the plan was built for another query group")
     if plan.dev is None:
         plan.to(q.device)
+        _hold(stream, dev, plan.dev_stream, plan.dev)
     if out is None:
         out = (torch.empty if N == plan.num_rows else torch.zeros)(shape, dtype=bf16, device=q.device)
         _record(stream, out)
