@@ -264,6 +264,7 @@ def rlt_publishable_prefix(written, page_size: int, out=None, stream=None):
     num_banks, batch = int(written.shape[0]), int(written.shape[1])
     if out is None:
         out = torch.empty(batch, dtype=torch.int32, device=written.device)
+        _record(stream, out)
     _check(load().rlt_publishable_prefix(_dev(written, torch.int32, "written") if num_banks else ctypes.c_void_p(0),
                                          num_banks, batch, int(page_size), _dev(out, torch.int32, "out"),
                                          _stream(stream)), "rlt_publishable_prefix")
@@ -316,9 +317,11 @@ def rlt_paged_decode_attn(pool: KVPool, bank: int, q, page_table, seq_lens, max_
     B, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
+        _record(stream, out)
     ws_need = rlt_paged_decode_workspace_size(B, Hq, pool.num_kv_heads, D, max_seq_len, split_tokens)
     if workspace is None and ws_need > 0:
         workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
+        _record(stream, workspace)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     lse_ptr = _dev(lse_out, torch.float32, "lse_out") if lse_out is not None else ctypes.c_void_p(0)
@@ -349,6 +352,7 @@ def rlt_paged_decode_attn_noalloc(pool: KVPool, bank: int, q, page_table, seq_le
     B, Hq, D = q.shape
     if out is None:
         out = torch.empty_like(q)
+        _record(stream, out)
     lse_ptr = _dev(lse_out, torch.float32, "lse_out") if lse_out is not None else ctypes.c_void_p(0)
     if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("page_table must be [B][max_pages] and seq_lens [B]")
@@ -373,6 +377,7 @@ def rlt_latent_noise_init(seeds, positions, channels: int, initializer_range: fl
         raise ValueError("seeds and positions must have one entry per row")
     if out is None:
         out = torch.empty((n, channels), dtype=torch.float32, device=seeds.device)
+        _record(stream, out)
     _check(load().rlt_latent_noise_init(_dev(out, torch.float32, "out"), _dev(seeds, torch.uint64, "seeds")
                                         if seeds.dtype == torch.uint64 else _dev(seeds, torch.int64, "seeds"),
                                         _dev(positions, torch.int64, "positions"), n, channels,
@@ -387,6 +392,7 @@ def rlt_noise_hash24(seeds, positions, channels: int, out=None, stream=None):
     n = int(seeds.numel())
     if out is None:
         out = torch.empty((n, channels), dtype=torch.int32, device=seeds.device)
+        _record(stream, out)
     _check(load().rlt_noise_hash24(_dev(out, torch.int32, "out"), _dev(seeds, seeds.dtype, "seeds"),
                                    _dev(positions, torch.int64, "positions"), n, channels,
                                    _stream(stream)), "rlt_noise_hash24")
@@ -401,8 +407,10 @@ def rlt_paged_gather(pool: KVPool, bank: int, page_table, seq_lens, max_len: int
     shape = (B, max_len, pool.num_kv_heads, pool.head_dim)
     if k_out is None:
         k_out = torch.zeros(shape, dtype=torch.bfloat16, device=pool.k.device)
+        _record(stream, k_out)
     if v_out is None:
         v_out = torch.zeros(shape, dtype=torch.bfloat16, device=pool.k.device)
+        _record(stream, v_out)
     _check(load().rlt_paged_gather(ctypes.byref(pool.struct), bank, _dev(page_table, torch.int32, "page_table"),
                                    page_table.shape[1], _dev(seq_lens, torch.int32, "seq_lens"), B,
                                    int(max_len), _dev(k_out, torch.bfloat16, "k_out"),
@@ -428,7 +436,7 @@ class PrefixPlan:
             self.max_members, self.max_rest_len, self.work_units = (int(x) for x in sizes)
         self.chunk_tiles = chunk_tiles
         self.query_group = query_group
-        self.dev = None
+        self.dev, self.dev_stream = None, None
 
     def to(self, device):
         import torch
@@ -436,6 +444,7 @@ class PrefixPlan:
             a = np.ascontiguousarray(a, np.int32).reshape(-1)
             return torch.from_numpy(a if a.size else np.zeros(1, np.int32)).to(device)
         self.dev = (t(self.segments), t(self.members), t(self.member_limit), t(self.request_prefix))
+        self.dev_stream = _current_stream_on(self.dev[0])
         return self
 
 
@@ -504,13 +513,16 @@ def rlt_paged_decode_attn_prefix(pool: KVPool, bank: int, q, page_table, seq_len
         raise ValueError("the plan was built for another query group")
     if plan.dev is None:
         plan.to(q.device)
+    _hold(stream, plan.dev_stream, *plan.dev)
     if out is None:
         out = torch.empty_like(q)
+        _record(stream, out)
     rest = plan.max_rest_len if plan.num_segments else int(max_seq_len)
     need = rlt_paged_decode_prefix_workspace_size(B, Hq, pool.num_kv_heads, D, rest,
                                                   plan.max_prefix_slots, split_tokens)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _record(stream, workspace)
     lse_ptr = _dev(lse_out, torch.float32, "lse_out") if lse_out is not None else ctypes.c_void_p(0)
     seg, mem, lim, req = plan.dev
     kn, vn = _new_rows(k_new, v_new, B, pool.num_kv_heads, D)
@@ -538,12 +550,13 @@ class ExtendPlan:
         (self.num_segments, self.num_rows, self.max_chunks, self.max_slots, self.max_members, _,
          self.work_units) = (int(x) for x in sizes)
         self.chunk_tiles, self.query_group = chunk_tiles, query_group
-        self.dev = None
+        self.dev, self.dev_stream = None, None
 
     def to(self, device):
         import torch
         self.dev = [torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(device)
                     for a in (self.segments, self.members, self.member_limit, self.row_prefix, self.row_len)]
+        self.dev_stream = _current_stream_on(self.dev[0])
         return self
 
 
@@ -586,11 +599,14 @@ def rlt_paged_extend_attn(pool: KVPool, bank: int, q, page_table, plan: ExtendPl
         raise ValueError("the plan was built for another query group")
     if plan.dev is None:
         plan.to(q.device)
+    _hold(stream, plan.dev_stream, *plan.dev)
     if out is None:
         out = torch.empty_like(q)
+        _record(stream, out)
     need = int(load().rlt_paged_extend_workspace_size(N, Hq, D, max(plan.max_slots, 1)))
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _record(stream, workspace)
     lse_ptr = _dev(lse_out, torch.float32, "lse_out") if lse_out is not None else ctypes.c_void_p(0)
     seg, mem, lim, rp, rl = plan.dev
     _check(load().rlt_paged_extend_attn(
@@ -663,15 +679,18 @@ def _device_index():
 
 
 def _record(stream, *made):
-    """Tensors this call made on torch's current stream and uses on `stream`: tell the allocator."""
+    """Tensors this call made on torch's current stream and uses on `stream`: it waits for that stream, and the allocator
+    keeps them until it is done with them."""
     import torch
-    if stream is None:
+    made = [t for t in made if t is not None]
+    if stream is None or not made:
         return
     s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if s.cuda_stream == _current_stream_on(made[0]):
+        return
+    s.wait_stream(torch.cuda.current_stream())
     for t in made:
-        if t is not None:
-            s.wait_stream(torch.cuda.current_stream())
-            t.record_stream(s)
+        t.record_stream(s)
 
 
 def _refuse(t, dtype, name, shape, dev):
@@ -852,17 +871,18 @@ def _current_stream_on(t):
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
 
 
-def _hold(stream, dev, made_on, *tensors):
+def _hold(stream, made_on, *tensors):
     """Arrays of a plan, uploaded on stream `made_on`, that a call is about to read on `stream`: where that is another one,
     the allocator keeps their memory until the call is done, also if the plan dies when the call returns."""
     import torch
-    raw = _raw_stream(stream, dev)
+    if not tensors[0].is_cuda:
+        return                                   # (refused by the call)
+    raw = _raw_stream(stream, tensors[0].get_device())
     if raw == made_on:
         return
     s = torch.cuda.ExternalStream(raw) if stream is None or isinstance(stream, int) else stream
     for t in tensors:
-        if t.is_cuda:
-            t.record_stream(s)
+        t.record_stream(s)
 
 
 def _np_ptr(a):
@@ -875,7 +895,7 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
     allowed), N >= the plan's rows; rows behind the last sequence are left alone (zeros in an out made here).
     A plan not uploaded yet is uploaded here (not under stream capture).  Returns out [N][Hq][D]."""
     if plan.dev is not None:
-        _hold(stream, _device_index(), plan.dev_stream, plan.dev)
+        _hold(stream, plan.dev_stream, plan.dev)
     st = (_bound or _plain()).prefill(q, k, v, plan.dev, plan.num_items, plan.num_rows, plan.max_key_tiles,
                                         plan.total_key_tiles, plan.query_group, out, lse_out, scale,
                                         ATTN_EARLY_START if early_start else 0, stream)
@@ -898,7 +918,7 @@ def rlt_prefill_attn(q, k, v, plan: PrefillPlan, out=None, lse_out=None, scale: 
         raise ValueError("the plan was built for another query group")
     if plan.dev is None:
         plan.to(q.device)
-        _hold(stream, dev, plan.dev_stream, plan.dev)
+        _hold(stream, plan.dev_stream, plan.dev)
     if out is None:
         out = (torch.empty if N == plan.num_rows else torch.zeros)(shape, dtype=bf16, device=q.device)
         _record(stream, out)
