@@ -23,6 +23,7 @@ Functions keep the C names:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import numpy as np
@@ -656,6 +657,16 @@ class KV8Pool:
 _bound = None
 
 
+class _NoMarshal:
+    """In the place of the C marshaller where it was not built for this Python: takes no call."""
+
+    @staticmethod
+    def append(*args):
+        return None
+
+    decode = prefill = append
+
+
 def _plain():
     """The C marshaller of calls in their plain form (csrc/marshal.c): its functions return the library's status, or
     None for any other call, which the Python code behind them checks and makes."""
@@ -663,7 +674,11 @@ def _plain():
     if _bound is None:
         import torch
 
-        from . import _marshal as m
+        try:
+            m = importlib.import_module("._marshal", __name__)
+        except ModuleNotFoundError:
+            _bound = _NoMarshal
+            return _bound
         at = lambda name: ctypes.cast(getattr(load(), name), ctypes.c_void_p).value      # noqa: E731
         m.bind(torch.Tensor, torch.bfloat16, torch.int32, torch.int64, torch.float32, torch._C._cuda_getDevice,
                torch._C._cuda_getCurrentRawStream, at("rlt_kv8_append_rope"), at("rlt_paged_decode_attn_kv8"),

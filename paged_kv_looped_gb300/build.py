@@ -1,5 +1,6 @@
 """Build librlt.so (sm_103a) in-tree with nvcc, one object per .cu, compiled in parallel, and the binding's
-argument marshaller (_marshal.so, C) with the host compiler."""
+argument marshaller (_marshal, a CPython module in C) with the host compiler where Python's headers are there: the
+binding does without it, a few microseconds a call slower."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -15,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librlt.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))   # this Python's alone
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,11 +36,40 @@ def _inputs() -> list[str]:
     return files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
 
 
+def _python_headers() -> str | None:
+    """The folder of this Python's headers, if it has them."""
+    include = sysconfig.get_paths()["include"]
+    return include if os.path.exists(os.path.join(include, "Python.h")) else None
+
+
+def _host_cc() -> str | None:
+    return shutil.which("gcc") or shutil.which("cc")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
+    made = [LIB] + ([MARSHAL] if _python_headers() and _host_cc() else [])
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def build_marshal() -> str | None:
+    """Compile csrc/marshal.c for this Python; None where its headers or a C compiler are missing."""
+    include, cc = _python_headers(), _host_cc()
+    if include is None or cc is None:
+        sys.stderr.write("paged_kv_looped_gb300: no Python headers or no C compiler; calls are marshalled in Python\n")
+        return None
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    r = subprocess.run([cc, "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE, "-I", include,
+                        os.path.join(CSRC, "marshal.c"), "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling marshal.c failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    untagged = os.path.join(PKG, "_marshal.so")  # one without an ABI tag, which any Python would load
+    if untagged != MARSHAL and os.path.exists(untagged):
+        os.remove(untagged)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -60,13 +90,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE,
-                        "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.c"), "-o", tmp],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"compiling marshal.c failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
+    build_marshal()
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources())) as ex:
         results = list(ex.map(compile_one, sources()))
     if verbose_ptxas:
