@@ -512,9 +512,10 @@ RLT_API rlt_status rlt_paged_gather(const rlt_kv_pool *pool, int32_t bank, const
  * largest magnitude (of the bf16 row handed in, for keys before their rotation),
  *     e = max(floor(log2 a) - 7, -64)      (0 for a row of zeros),
  *     held = e4m3(x * 2^-e), nearest even;  the exponent array holds e + 127;
- * the row stands for held * 2^e.  A finite row never saturates.  A row with an
- * infinity or NaN gets e = 121 (infinities held as 448, NaN as NaN).  Held rows
- * are exact in bf16.  The pages' engines keep bf16; this format is the library's own.
+ * the row stands for held * 2^e.  A finite row does not saturate, and held rows are exact in
+ * bf16, while every held magnitude is below 1.9375 * 2^127 (for keys: every rotated pair's norm);
+ * from there on a value is held as 2^128, an infinity in bf16.  A row with an
+ * infinity or NaN gets e = 121 (infinities held as 448, NaN as NaN).  The pages' engines keep bf16; this format is the library's own.
  * Pages, slots, page tables and banks as in rlt_kv_pool.
  */
 typedef struct rlt_kv8_pool {

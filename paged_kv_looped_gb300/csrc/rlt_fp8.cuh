@@ -4,8 +4,8 @@
 // magnitude (before the rotation, for keys),
 //     e = max(floor(log2 a) - 7, -64)   (0 for a row of zeros),   held = e4m3(x * 2^-e),
 // kept as the byte e + 127.  |x * 2^-e| < 2^8 for the row itself and < 2^8.5 = 362 after
-// a rotation (a pair's larger member grows by at most sqrt 2), below e4m3's 448: a finite
-// row never saturates.  The scale is a power of two, so a held value has four significant
+// a rotation (a pair's larger member grows by at most sqrt 2), below e4m3's 448: a
+// row does not saturate (up to 1.9375 * 2^127, where the value itself leaves fp32's range).  The scale is a power of two, so a held value has four significant
 // bits and is exact in bf16 and fp16, and the scale follows from the bf16 input bits
 // alone: two kernels (or a kernel and a reference) cannot disagree about it.  e4m3 floats, so
 // a scale that is not the tightest one loses no precision in its normal range, 2^-6..448
