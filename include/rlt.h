@@ -617,8 +617,8 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
  *   lse_out    fp32 [num_rows][num_q_heads], natural log, or NULL
  *   flags      0 or RLT_ATTN_EARLY_START (no kernel still running ahead may write items)
  * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
- * fp32; weights enter the product with V as bf16, up to 2^8 (values up to 2^119 cannot
- * overflow by it).  An infinity or NaN in q, k or v reaches the rows whose formula it is
+ * fp32; weights enter the product with V as bf16, up to 2^8 (a row's products are summed before they are
+ * divided by its weights: values below 2^120 / (number of its keys) cannot overflow by it).  An infinity or NaN in q, k or v reaches the rows whose formula it is
  * part of and no other: not earlier rows, not other sequences (an infinity whose weight is
  * below fp32's smallest as an infinity or a NaN, the same one every time).
  */
