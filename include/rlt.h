@@ -647,14 +647,16 @@ RLT_API rlt_status rlt_validate_batch(const int32_t *page_table, int32_t max_pag
 /*
  * Fault injection for tests of the bounded copy waits; the pages have no
  * counterpart (it exists so that the give-up path can be exercised without a
- * GPU fault).  Arms the next rlt_paged_decode_attn call made by this host
- * thread, once: its split-K kernel gives every copy wait wait_limit_ns (1 ns ..
- * 1 s; the ordinary limit is 1 s) and never issues the first tile copy of warp 0
- * of the CTA for (split 0, kv head 0, request 0), so that wait runs out.  The
- * kernel then records RLT_DEVERR_TIMEOUT, waits (bounded by the same limit) for
- * that warp's copies still in flight, leaves the warp's tiles out of request 0's
- * result for kv head 0's query heads, and returns: nothing faults or hangs, and
- * later calls are unaffected.  RLT_ERR_INVALID_ARG for a limit outside that range.
+ * GPU fault).  Arms the next rlt_paged_decode_attn, rlt_paged_decode_attn_kv8 or
+ * rlt_prefill_attn call made by this host
+ * thread, once: its kernel gives every copy wait wait_limit_ns (1 ns ..
+ * 1 s; the ordinary limit is 1 s) and never issues one copy, so that wait runs out.  The
+ * kernel then records RLT_DEVERR_TIMEOUT, waits (bounded) for the copies still in flight
+ * and returns: nothing faults or hangs, and later calls are unaffected.
+ * The decode kernels leave out the first tile copy of warp 0 of the CTA for (split 0, kv
+ * head 0, request 0), and that warp's tiles of request 0's result for kv head 0's query
+ * heads; the prompt kernel the first values of its block 0, which then writes nothing for the
+ * plan's first item and its unit of heads (nor for what else that block had taken over).  RLT_ERR_INVALID_ARG for a limit outside that range.
  */
 RLT_API rlt_status rlt_debug_fault_next_decode(uint64_t wait_limit_ns);
 

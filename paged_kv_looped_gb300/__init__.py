@@ -227,8 +227,8 @@ def rlt_get_device_error() -> int:
 
 
 def rlt_debug_fault_next_decode(wait_limit_ns: int):
-    """Test hook: the next rlt_paged_decode_attn of this thread runs with this copy-wait limit and
-    one tile copy left unissued, so that a wait runs out (see include/rlt.h)."""
+    """Test hook: the next rlt_paged_decode_attn, rlt_paged_decode_attn_kv8 or rlt_prefill_attn of this thread runs with
+    this copy-wait limit and one tile copy left unissued, so that a wait runs out (see include/rlt.h)."""
     _check(load().rlt_debug_fault_next_decode(int(wait_limit_ns)), "rlt_debug_fault_next_decode")
 
 

@@ -108,8 +108,8 @@ int64_t bank_elems(const rlt_kv_pool *pool)
 
 rlt_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RLT_OK : RLT_ERR_CUDA; }
 
-// rlt_debug_fault_next_decode: copy-wait limit (ns) for the next rlt_paged_decode_attn call of
-// this host thread, which also leaves one tile copy unissued; 0 = not armed.
+// rlt_debug_fault_next_decode: copy-wait limit (ns) for the next call of this host thread that takes it, which
+// also leaves one tile copy unissued; 0 = not armed.
 thread_local uint64_t t_fault_wait_ns = 0;
 
 }  // namespace
@@ -202,6 +202,13 @@ rlt_status check_slots(const int64_t *out_loc, int32_t n_tokens, int64_t num_slo
 }  // namespace
 
 namespace rlt {
+
+uint64_t take_fault_limit()
+{
+    const uint64_t limit = t_fault_wait_ns;
+    t_fault_wait_ns = 0;
+    return limit;
+}
 
 rlt_status current_device_info(unsigned int **err, int *num_sms) { return device_info(err, num_sms); }
 
@@ -444,11 +451,8 @@ RLT_API rlt_status rlt_paged_decode_attn(const rlt_kv_pool *pool, int32_t bank, 
     p.part_stride = plan.max_splits;
     const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)pool->head_dim);
     p.qscale = (float)(s * 1.4426950408889634);   // log2(e): softmax in base 2
-    if (t_fault_wait_ns != 0) {                   // armed by rlt_debug_fault_next_decode
-        p.wait_limit_ns = t_fault_wait_ns;
+    if ((p.wait_limit_ns = rlt::take_fault_limit()) != 0)
         p.debug_drop_copy = 1;
-        t_fault_wait_ns = 0;
-    }
     return from_cuda(rlt::launch_decode(p, pool->head_dim, group, static_cast<cudaStream_t>(stream),
                                         (flags & RLT_ATTN_EARLY_START) != 0));
 }

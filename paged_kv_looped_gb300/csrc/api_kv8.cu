@@ -207,6 +207,8 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
     p.tiles_per_split = plan.tiles_per_split;
     p.max_splits = plan.max_splits;
     p.part_stride = plan.max_splits;
+    if ((p.wait_limit_ns = rlt::take_fault_limit()) != 0)
+        p.debug_drop_copy = 1;
     const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)pool->head_dim);
     p.qscale = (float)(s * 1.4426950408889634);   // log2(e): softmax in base 2
     return from_cuda(rlt::launch_kv8_decode(p, b8, pool->head_dim, static_cast<cudaStream_t>(stream),
@@ -259,6 +261,7 @@ RLT_API rlt_status rlt_prefill_attn(const void *q, int32_t num_q_heads, int64_t 
     p.num_items = num_items;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
+    p.wait_limit_ns = rlt::take_fault_limit();
     const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)head_dim);
     p.qscale = (float)(s * 1.4426950408889634);   // log2(e): softmax in base 2
     return from_cuda(rlt::launch_prefill(p, head_dim, static_cast<cudaStream_t>(stream),

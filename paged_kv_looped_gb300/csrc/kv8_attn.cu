@@ -117,7 +117,8 @@ __device__ __forceinline__ int chunk_offset(int r, int c)
         return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D>
+// kFault: the timeout test's instance (rlt_debug_fault_next_decode): one copy left unissued, the limit from the call.
+template <int D, bool kFault>
 __global__ void __launch_bounds__(kThreads, 3)
     kv8_partial_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const DecodeParams p, const uint8_t *__restrict__ k_exp, const uint8_t *__restrict__ v_exp, int early)
@@ -197,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (lane / kStageTiles == i && my_row >= 0) {
             unsigned char *dst = pipe + (i % kStages) * C::kStageBytes + (lane % kStageTiles) * C::kTileBytes;
             uint8_t *de = exps + (i % kStages) * 2 * kStageTokens + (lane % kStageTiles) * kTileTokens;
-            tc::tma_load_2d_once(dst, &kmap, 0, my_row, bar);
+            if (!(kFault && i == 0 && lane == 0 && warp == 0 && split == 0 && head == 0 && b == 0))
+                tc::tma_load_2d_once(dst, &kmap, 0, my_row, bar);
             tc::tma_load_2d_once(dst + C::kSideBytes, &vmap, 0, my_row, bar);
             bulk_load_once(de, k_exp + my_row, kTileTokens, bar);
             bulk_load_once(de + kStageTokens, v_exp + my_row, kTileTokens, bar);
@@ -247,12 +249,13 @@ __global__ void __launch_bounds__(kThreads, 3)
 
     const int tok_g = token_of<D>(g);            // this lane's tokens of a tile's scores: tok_g, tok_g + 8
     const int tok_a = token_of<D>(2 * t), tok_b = token_of<D>(2 * t + 1);   // and of its values (and + 8)
+    const uint64_t limit = kFault ? p.wait_limit_ns : kWaitLimitNs;
     uint32_t phase = 0;
     bool failed = false;
     int i = 0;
     for (; i < my_count; ++i) {
         const int s = i % kStages;
-        if (!__all_sync(kFullMask, mbar_wait(&bars[s], (phase >> s) & 1u))) {
+        if (!__all_sync(kFullMask, mbar_wait(&bars[s], (phase >> s) & 1u, limit))) {
             failed = true;
             break;
         }
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (lane == 0)
             record_error(p.err, RLT_DEVERR_TIMEOUT);
         for (int k = i; k < issued; ++k) {
-            mbar_wait(&bars[k % kStages], (phase >> (k % kStages)) & 1u);
+            mbar_wait(&bars[k % kStages], (phase >> (k % kStages)) & 1u, limit);
             phase ^= 1u << (k % kStages);
         }
         m0 = m1 = -CUDART_INF_F;
@@ -571,7 +574,7 @@ bool make_map8(CUtensorMap *map, const uint8_t *bank, int64_t rows, int head_dim
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kFault>
 cudaError_t launch_typed8(const DecodeParams &p, const Kv8Bank &bank, cudaStream_t stream, bool early)
 {
     using C = Cfg8<D>;
@@ -588,12 +591,12 @@ cudaError_t launch_typed8(const DecodeParams &p, const Kv8Bank &bank, cudaStream
         return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(kv8_partial_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        e = cudaFuncSetAttribute(kv8_partial_kernel<D, kFault>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
         if (e != cudaSuccess)
             return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    e = launch_kernel(kv8_partial_kernel<D>, dim3(p.max_splits, p.num_kv_heads, p.batch), dim3(kThreads),
+    e = launch_kernel(kv8_partial_kernel<D, kFault>, dim3(p.max_splits, p.num_kv_heads, p.batch), dim3(kThreads),
                       C::kSmemBytes, stream, true, kmap, vmap, p, bank.k_exp, bank.v_exp, early ? 1 : 0);
     if (e != cudaSuccess || p.max_splits <= 1)
         return e;
@@ -613,7 +616,11 @@ bool kv8_decode_supported(int head_dim, int group)
 
 cudaError_t launch_kv8_decode(const DecodeParams &p, const Kv8Bank &bank, int head_dim, cudaStream_t stream, bool early)
 {
-    return head_dim == 128 ? launch_typed8<128>(p, bank, stream, early) : launch_typed8<64>(p, bank, stream, early);
+    if (p.debug_drop_copy != 0)
+        return head_dim == 128 ? launch_typed8<128, true>(p, bank, stream, early)
+                               : launch_typed8<64, true>(p, bank, stream, early);
+    return head_dim == 128 ? launch_typed8<128, false>(p, bank, stream, early)
+                           : launch_typed8<64, false>(p, bank, stream, early);
 }
 
 }  // namespace rlt

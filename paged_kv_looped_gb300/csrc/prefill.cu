@@ -143,9 +143,9 @@ __device__ __forceinline__ int answered_block(const void *answer)
     return got != 0 ? x : -1;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const volatile int *abort)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const volatile int *abort, uint64_t limit)
 {
-    return __all_sync(kFullMask, mbar_wait_or_abort(bar, parity, abort));
+    return __all_sync(kFullMask, mbar_wait_or_abort(bar, parity, abort, limit));
 }
 
 // 2^x, kept in program order among volatile instructions.
@@ -167,7 +167,8 @@ __device__ __forceinline__ void store_sector(void *dst, const uint32_t (&y)[8])
 // Whether a word of two bf16 values holds an infinity or NaN, from the larger magnitude's bits.
 __device__ __forceinline__ bool not_finite(uint32_t bits) { return (bits & 0xffffu) >= 0x7f80u || bits >= 0x7f800000u; }
 
-template <int D>
+// kFault: the timeout test's instance (rlt_debug_fault_next_decode): one copy left unissued, the limit from the call.
+template <int D, bool kFault>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tslot;
     bool ok = true;
+    const uint64_t limit = kFault ? p.wait_limit_ns : kWaitLimitNs;
 
     // Every role goes through the same works; key tiles of tile s: up to its last row's own key.
     auto take = [&](int d, Work &w) {            // (the barrier has been waited for)
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool asked = false;
             uint32_t parity = 1;                 // of the slot's previous release (none in the first round)
             for (int d = 0;; ++d) {
-                if (d >= 2 && !(ok = mbar_wait_or_abort(&bars[C::kWorkFree + (d & 1)], (d / 2 - 1) & 1u, abort_flag)))
+                if (d >= 2 && !(ok = mbar_wait_or_abort(&bars[C::kWorkFree + (d & 1)], (d / 2 - 1) & 1u, abort_flag, limit)))
                     break;
                 Work w{0, -1, 0, 0};
                 if (block >= 0) {
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n = max(key_tiles(w, 0), key_tiles(w, 1));
                 for (int i = 0; ok && i < 2 * n; ++i) {
                     if (i < 2) {
-                        if (d > 0 && !(ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag)))
+                        if (d > 0 && !(ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag, limit)))
                             break;
                         if (key_tiles(w, i) > 0) {
                             load(base + i * C::kTileBytes, &qmap, head0 + i * head_step, w.row0 + w.q0 + i * tok_step,
@@ -310,10 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive(&bars[C::kQFull + i]);
                         }
                     }
-                    if (issued >= C::kStages && !(ok = mbar_wait_or_abort(&bars[C::kFree + st], parity, abort_flag)))
+                    if (issued >= C::kStages && !(ok = mbar_wait_or_abort(&bars[C::kFree + st], parity, abort_flag, limit)))
                         break;
-                    load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head,
-                         w.row0 + (i >> 1) * kTile, &bars[C::kFull + st]);
+                    if (kFault && blockIdx.x == 0 && d == 0 && i == 1)
+                        mbar_arrive_expect_tx(&bars[C::kFull + st], C::kTileBytes);   // these bytes never arrive
+                    else
+                        load(base + C::kRingOff + st * C::kTileBytes, (i & 1) ? &vmap : &kmap, kv_head,
+                             w.row0 + (i >> 1) * kTile, &bars[C::kFull + st]);
                     ++issued;
                     if (++st == C::kStages) {
                         st = 0;
@@ -323,11 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n == 0) {                    // (keeps the Q barriers' phases one a work)
                     for (int i = 0; ok && i < 2; ++i) {
                         if (d > 0)
-                            ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag);
+                            ok = mbar_wait_or_abort(&bars[C::kQFree + i], (d - 1) & 1u, abort_flag, limit);
                         mbar_arrive(&bars[C::kQFull + i]);
                     }
                 }
-                if (!ok || !(ok = mbar_wait_or_abort(&bars[C::kNext], d & 1u, abort_flag)))
+                if (!ok || !(ok = mbar_wait_or_abort(&bars[C::kNext], d & 1u, abort_flag, limit)))
                     break;
                 asked = false;
                 block = answered_block(base + C::kNextOff);
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // every copy and the scheduler's answer have landed before the CTA gives up its memory (bounded;
                 // on the normal path the other roles have waited for all of them)
                 for (int i = max(0, issued - C::kStages); i < issued; ++i)
-                    mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u);
+                    mbar_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, limit);
                 for (uint64_t t0 = global_ns(); (asked || queries[0] || queries[1]) && global_ns() - t0 < kWaitLimitNs / 100;)
                     ;
             }
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t parity = 0;
             auto wait_slot = [&](int &slot) -> bool {
                 slot = st;
-                if (!mbar_wait_or_abort(&bars[C::kFull + st], parity, abort_flag))
+                if (!mbar_wait_or_abort(&bars[C::kFull + st], parity, abort_flag, limit))
                     return false;
                 if (++st == C::kStages) {
                     st = 0;
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto pass_turn = [&]() { *turn = 0; };
             int tiles = 0, items = 0, s_issued = 0;   // key tiles and works with rows, over all works
             for (int d = 0;; ++d) {
-                if (!(ok = mbar_wait_or_abort(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag)))
+                if (!(ok = mbar_wait_or_abort(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag, limit)))
                     break;
                 Work w;
                 take(d, w);
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int ns0 = key_tiles(w, 0), ns = key_tiles(w, s), n = max(ns0, key_tiles(w, 1));
                 uint64_t *clean = &bars[C::kClean + (d & 1) * 2];
                 int k_slot = 0, v_slot = 0;
-                if (!(ok = mbar_wait_or_abort(&bars[C::kQFull + s], d & 1u, abort_flag)))
+                if (!(ok = mbar_wait_or_abort(&bars[C::kQFull + s], d & 1u, abort_flag, limit)))
                     break;
                 if (n > 0) {
                     if (!(ok = wait_slot(k_slot)))
@@ -441,22 +446,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j < ns) {
                         // The values of the last keys have been looked at: a pair's tiles share them, and at an odd group
                         // tile 0's last keys are ordinary ones of tile 1.  (Waited for before the turn is taken.)
-                        if (j == ns0 - 1 && !(ok = mbar_wait_or_abort(&clean[0], (d / 2) & 1u, abort_flag)))
+                        if (j == ns0 - 1 && !(ok = mbar_wait_or_abort(&clean[0], (d / 2) & 1u, abort_flag, limit)))
                             break;
                         if (!pair && s == 1 && j == ns - 1 &&
-                            !(ok = mbar_wait_or_abort(&clean[1], (d / 2) & 1u, abort_flag)))
+                            !(ok = mbar_wait_or_abort(&clean[1], (d / 2) & 1u, abort_flag, limit)))
                             break;
                         // the item before has left O
                         if (j == 0 && items > 0 &&
-                            !(ok = mbar_wait_or_abort(&bars[C::kOFree + s], (items - 1) & 1u, abort_flag)))
+                            !(ok = mbar_wait_or_abort(&bars[C::kOFree + s], (items - 1) & 1u, abort_flag, limit)))
                             break;
-                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], tiles & 1u, abort_flag)))
+                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s], tiles & 1u, abort_flag, limit)))
                             break;
                         if (!(ok = take_turn()))
                             break;
                         tc::fence_after_sync();
                         issue_pv(0, v_slot, j == 0);
-                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], tiles & 1u, abort_flag)))
+                        if (!(ok = mbar_wait_or_abort(&bars[C::kPFull + 2 * s + 1], tiles & 1u, abort_flag, limit)))
                             break;
                         tc::fence_after_sync();
                         issue_pv(1, v_slot, false);
@@ -486,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // last ODone covers all; after an abort, the last S and some time for a P V half behind it
             if (ok) {
                 if (items > 0)
-                    mbar_wait(&bars[C::kODone + s], (items - 1) & 1u);
+                    mbar_wait(&bars[C::kODone + s], (items - 1) & 1u, limit);
             } else {
                 if (s_issued > 0)
-                    mbar_wait(&bars[C::kSFull + s], (s_issued - 1) & 1u);
+                    mbar_wait(&bars[C::kSFull + s], (s_issued - 1) & 1u, limit);
                 for (uint64_t t0 = global_ns(); global_ns() - t0 < kWaitLimitNs / 100;)
                     ;
             }
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int tiles = 0, items = 0, copies = 0;    // of this tile, and of the ring before this work
         for (int d = 0;; ++d) {
-            if (!(ok = warp_wait(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag)))
+            if (!(ok = warp_wait(&bars[C::kWorkFull + (d & 1)], (d / 2) & 1u, abort_flag, limit)))
                 break;
             Work wk;
             take(d, wk);
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // 32 rows of the tile's own, a lane a row.  (One further warp for all of it took 321 us where this
                     // takes 298, 16 prompts of 1024-2000 tokens x 32 heads.)
                     const int i = copies + 2 * j + 1;
-                    if (!(ok = warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag)))
+                    if (!(ok = warp_wait(&bars[C::kFull + i % C::kStages], (i / C::kStages) & 1u, abort_flag, limit)))
                         break;
                     unsigned char *vt = base + C::kRingOff + i % C::kStages * C::kTileBytes;
                     const int r = pair ? warp * 16 + (lane >> 1) : quarter * 32 + lane;
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0)
                         mbar_arrive(&bars[C::kClean + (d & 1) * 2 + (pair ? 0 : s)]);
                 }
-                if (!(ok = warp_wait(&bars[C::kSFull + s], tiles & 1u, abort_flag)))
+                if (!(ok = warp_wait(&bars[C::kSFull + s], tiles & 1u, abort_flag, limit)))
                     break;
                 tc::fence_after_sync();
                 // P = 2^(s - m), 32 columns at a time.  The exponentials of the next columns are issued ahead of the
@@ -702,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 sum = f2_unpack(f2_add(sum2[0], sum2[1]));
                 l_run += sum.x + sum.y;
             }
-            if (ok && ns > 0 && (ok = warp_wait(&bars[C::kODone + s], items & 1u, abort_flag))) {
+            if (ok && ns > 0 && (ok = warp_wait(&bars[C::kODone + s], items & 1u, abort_flag, limit))) {
                 tc::fence_after_sync();
                 ++items;
                 const float inv = 1.f / l_run;
@@ -819,7 +824,7 @@ bool make_rows_map(CUtensorMap *map, const uint16_t *ptr, int64_t rows, int head
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kFault>
 cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bool early)
 {
     using C = PCfg<D>;
@@ -837,7 +842,7 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
         return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     if (bit == 0 || (configured.load(std::memory_order_acquire) & bit) == 0) {
-        e = cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(prefill_kernel<D, kFault>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess)
             return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
@@ -855,7 +860,7 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
     PrefillParams c = p;
     c.chunk_units = (int32_t)kv_heads * per_kv;
     c.early = early ? 1 : 0;
-    return launch_kernel(prefill_kernel<D>, dim3(p.num_items * per_kv * p.num_kv_heads), dim3(kThreads), C::kSmem,
+    return launch_kernel(prefill_kernel<D, kFault>, dim3(p.num_items * per_kv * p.num_kv_heads), dim3(kThreads), C::kSmem,
                          stream, true, qmap, kmap, vmap, omap, c);
 }
 
@@ -863,7 +868,11 @@ cudaError_t launch_prefill_typed(const PrefillParams &p, cudaStream_t stream, bo
 
 cudaError_t launch_prefill(const PrefillParams &p, int head_dim, cudaStream_t stream, bool early)
 {
-    return head_dim == 128 ? launch_prefill_typed<128>(p, stream, early) : launch_prefill_typed<64>(p, stream, early);
+    if (p.wait_limit_ns != 0)
+        return head_dim == 128 ? launch_prefill_typed<128, true>(p, stream, early)
+                               : launch_prefill_typed<64, true>(p, stream, early);
+    return head_dim == 128 ? launch_prefill_typed<128, false>(p, stream, early)
+                           : launch_prefill_typed<64, false>(p, stream, early);
 }
 
 }  // namespace rlt

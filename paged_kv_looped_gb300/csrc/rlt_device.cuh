@@ -175,7 +175,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 // As mbar_wait, but also gives up as soon as *abort turns non-zero (another
 // role of the CTA gave up first).
 __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parity,
-                                                   const volatile int *abort)
+                                                   const volatile int *abort, uint64_t limit_ns = kWaitLimitNs)
 {
     if (mbar_try_wait(bar, parity))
         return true;
@@ -183,7 +183,7 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t *bar, uint32_t parit
     for (uint32_t it = 1; it != 0; ++it) {
         if (mbar_try_wait(bar, parity))
             return true;
-        if ((it & 63u) == 0u && (*abort != 0 || global_ns() - t0 > kWaitLimitNs))
+        if ((it & 63u) == 0u && (*abort != 0 || global_ns() - t0 > limit_ns))
             return false;
     }
     return false;

@@ -174,6 +174,9 @@ cudaError_t launch_noise(float *out, uint32_t *hash_out, const uint64_t *seeds,
                          const int64_t *positions, int64_t n_rows, int32_t channels,
                          float initializer_range, cudaStream_t stream);
 
+// The wait limit that rlt_debug_fault_next_decode armed this host thread's next call with, once; 0: not armed.
+uint64_t take_fault_limit();
+
 // Error word and SM count of the current device (looked up once per device).
 rlt_status current_device_info(unsigned int **err, int *num_sms);
 
@@ -240,6 +243,8 @@ struct PrefillParams {
     int32_t chunk_units;         // units of heads that run through the items together (launch_prefill sets it)
     int32_t early;               // items may be read before the kernels ahead have completed (launch_prefill sets it)
     float qscale;                // softmax scale * log2(e)
+    uint64_t wait_limit_ns;      // non-zero: the fault instance (rlt_debug_fault_next_decode), whose block 0 never issues
+                                 // the copy of its first values
 };
 
 cudaError_t launch_prefill(const PrefillParams &p, int head_dim, cudaStream_t stream, bool early);
