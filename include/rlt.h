@@ -617,10 +617,11 @@ RLT_API rlt_status rlt_paged_decode_attn_kv8(const rlt_kv8_pool *pool, int32_t b
  *   lse_out    fp32 [num_rows][num_q_heads], natural log, or NULL
  *   flags      0 or RLT_ATTN_EARLY_START (no kernel still running ahead may write items)
  * Supported: head_dim 64 or 128, any whole num_q_heads / num_kv_heads.  Scores and sums are
- * fp32; weights enter the product with V as bf16, up to 2^8 (a row's products are summed before they are
- * divided by its weights: values below 2^120 / (number of its keys) cannot overflow by it).  An infinity or NaN in q, k or v reaches the rows whose formula it is
- * part of and no other: not earlier rows, not other sequences (an infinity whose weight is
- * below fp32's smallest as an infinity or a NaN, the same one every time).
+ * fp32; weights enter the product with V as bf16, up to 2^8 (a row's products are summed before
+ * they are divided by its weights: values below 2^120 / (number of its keys) cannot overflow by
+ * it).  An infinity or NaN in q, k or v reaches the rows whose formula it is part of and no
+ * other: not earlier rows, not other sequences (an infinity whose weight is below fp32's smallest
+ * as an infinity or a NaN, the same one every time).
  */
 RLT_API rlt_status rlt_plan_prefill(const int32_t *seq_lens, int32_t batch, int32_t query_group, int32_t *items,
                                     int32_t max_items, int32_t *sizes);
@@ -656,7 +657,8 @@ RLT_API rlt_status rlt_validate_batch(const int32_t *page_table, int32_t max_pag
  * The decode kernels leave out the first tile copy of warp 0 of the CTA for (split 0, kv
  * head 0, request 0), and that warp's tiles of request 0's result for kv head 0's query
  * heads; the prompt kernel the first values of its block 0, which then writes nothing for the
- * plan's first item and its unit of heads (nor for what else that block had taken over).  RLT_ERR_INVALID_ARG for a limit outside that range.
+ * plan's first item and its unit of heads (nor for what else that block had taken over).
+ * RLT_ERR_INVALID_ARG for a limit outside that range.
  */
 RLT_API rlt_status rlt_debug_fault_next_decode(uint64_t wait_limit_ns);
 

@@ -110,7 +110,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8], float by)
 // angles are computed once and used for every head; the rows of kBatch rounds are loaded before the
 // first is worked on.  Bound by memory: 2 (hq + 2 hkv) D bytes in, as many out, and the cache: 16389 tokens
 // of 64 + 16 heads (705 MB) 115 us, 6.1 TB/s (a copy's rate is 6.7).  Rounds: 3 and 4 take 115 us
-// here, 26 and 29 us for 16000 tokens of 6 + 4 heads (before the angles were shared: 2 rounds 125 us where 4
+// here, 27 and 29 us for 16000 tokens of 6 + 4 heads (90 MB, 13.5 us of bytes: a warp's one round of rows leaves
+// nothing in flight while it is worked on; before the angles were shared: 2 rounds 125 us where 4
 // took 118).  A lane computing all its eight angles itself took 118 and 34 us, a kernel of one row a warp 863.
 constexpr int kBatch = 3;
 
@@ -255,7 +256,7 @@ __device__ __forceinline__ void store_words(uint16_t *row, int lane, const uint3
 
 // Any even rot_dim: a row passes through shared memory, where a lane finds the other member of its pairs.
 // A warp stays with one token; its angles (at most two pairs a lane) are computed once.  16000 tokens of 32 + 16
-// heads at rot_dim 62 (426 MB) 104 us; one row at a time took 128.
+// heads at rot_dim 62 (426 MB, 64 us of bytes) 105 us; one row at a time took 128.
 template <int D>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv8_append_pairs_kernel(const Kv8AppendParams p, int splits)
 {

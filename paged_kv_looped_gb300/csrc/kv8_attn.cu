@@ -17,7 +17,7 @@
 // and 8-bit operands on both sides.)
 //   S^T = K q^T   A = 16 tokens x 16 dims, e4m3 -> fp16 in registers (exact); B = the queries,
 //                 fp16 after a power-of-two scale per head that brings the head's largest
-//                 magnitude into [2^14, 2^15) (a bf16 query is exact there down to 2^-38 of it)
+//                 magnitude into [2^14, 2^15) (a bf16 query keeps its bits there down to 2^-38 of it)
 //   O^T = V^T P^T A = 16 dims x 16 tokens, pairs of tokens interleaved byte by byte; B = P^T,
 //                 S^T's accumulator transposed by movmatrix.  P is rounded to fp16 (2^-11
 //                 relative down to 2^-28 of the largest weight, thanks to the 2^14 above)
@@ -26,12 +26,14 @@
 // tiles land swizzled by the tensor copy (16-byte chunks XORed by row), and the token order below
 // makes the reads of both K and V free of bank conflicts at head_dim 128.
 //
-// Measured: 64 requests x 16 kv heads x 512-4096 tokens (599 MB) 97 us, 256 log-normal requests x 8 (1.84 GB)
-// 275 us, 8 x 32k-131k tokens x 8 (1.16 GB) 178 us with the join.  While the SMs are busy the cache comes in at
-// 6.65 TB/s (a copy's rate is 6.7); what is left is the grid's start and its last CTAs (7 us).
-// Three CTAs an SM with two stages of two tiles a warp; calls in a row, launched only at the end of the kernel
-// ahead, took 100 / 275 / 178 us with them, 118 / 318 / 198 with two CTAs of three such stages, 110 / 301 / 190
-// with four stages of one tile, 101 / 277 / 181 with four CTAs of three stages of one tile.
+// Measured: 64 requests x 16 kv heads x 512-4096 tokens (599 MB) 98.6 us, 256 log-normal requests x 8 (1.84 GB)
+// 279.5 us, 8 x 32k-131k tokens x 8 (1.16 GB) 180.3 us with the join: 91, 98 and 96 % of a copy's 6.7 TB/s; what is
+// left of the first is the grid's start and its last CTAs (7 us).  At head_dim 64 a tile is 2 KB for the same
+// copies and instructions: 302 MB in 67.5 us (4.5 TB/s), 928 MB in 181 (5.1).
+// Three CTAs an SM with two stages of two tiles a warp; in an earlier form, whose calls in a row started only at the
+// end of the kernel ahead, they took 100 / 275 / 178 us, 118 / 318 / 198 with two CTAs of three such stages,
+// 110 / 301 / 190 with four stages of one tile, 101 / 277 / 181 with four CTAs of three stages of one tile.
+// The zero rows' look costs 0.3 to 0.6 %; at every tile, not only where the maximum rises, it took 1 to 1.7 %.
 #include <cuda.h>
 #include <math_constants.h>
 

@@ -14,9 +14,9 @@
 // 4 * 128 * 128 * head_dim flops a tile and key tile take the tensor pipe 1024 clocks at head_dim 128.
 // A tile's chain (softmax, then P V and the next S, and the hand-overs between them) takes 2600 clocks where
 // two tiles' products alone would take 2048, so the chain bounds long prompts, the tensor pipe 80 %
-// busy: 15973 tokens x 64 heads 2514 us (1660 TFLOP/s, 84 % of a large cuBLAS product's measured rate).
+// busy: 15973 tokens x 64 heads 2510-2575 us (1620-1665 TFLOP/s, 82-84 % of a large cuBLAS product's measured rate).
 // Short prompts lose more to each item's first and last key tiles, whose chain is half empty (16 prompts
-// of 1024-2000 tokens x 32 heads: 295 us, 980 TFLOP/s, tensor pipe 52 % busy).
+// of 1024-2000 tokens x 32 heads: 294-302 us, 955-980 TFLOP/s, tensor pipe 52 % busy).
 //
 // Roles: warps 0-3 / 4-7 softmax of tile 0 / 1 (a thread owns one row = one tensor-memory lane: row maxima and
 // sums need no exchange), warp 8 / 9 the MMAs of tile 0 / 1, warp 10 the works and the copies.  The CTAs are
@@ -25,6 +25,10 @@
 // heads 351 -> 333 us; 16 prompts of 1024-2000 tokens 407 -> 328).  P (bf16) is written over the S
 // it came from, in two halves that the products take one by one.  The reference maximum of a row moves only when
 // the running maximum exceeds it by 2^8, so O is rescaled rarely, by the row's own thread.
+// P in bf16 is the one rounding besides the output's (both operands of a product have one type, and V is bf16): outputs
+// are off by 0.0019-0.0020 of themselves where fp32 weights leave 0.0015-0.0016.  The weights' sum is fp32, taken before
+// their rounding: taken after it, it would cost the softmax two more instructions a pair, and help only rows in which
+// one weight outweighs the rest.
 //
 // Tried and slower or equal at 8192 tokens x 32 heads: polling instead of suspended waits in the MMA threads
 // (351 -> 419 us), no maximum but a limit on the weights' sum (376), one MMA thread for both tiles (350), the
