@@ -695,7 +695,7 @@ def _device_index():
 
 def _record(stream, *made):
     """Tensors this call made on torch's current stream and uses on `stream`: it waits for that stream, and the allocator
-    keeps them until it is done with them."""
+    keeps them until it is done with them (so a raw handle has to stay a stream's as long as they live)."""
     import torch
     made = [t for t in made if t is not None]
     if stream is None or not made:
@@ -703,7 +703,11 @@ def _record(stream, *made):
     s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
     if s.cuda_stream == _current_stream_on(made[0]):
         return
-    s.wait_stream(torch.cuda.current_stream())
+    here = torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(s):
+        there = torch.cuda.is_current_stream_capturing()
+    if here == there:                            # (a captured stream cannot wait for one that is not, nor the reverse)
+        s.wait_stream(torch.cuda.current_stream())
     for t in made:
         t.record_stream(s)
 

@@ -101,3 +101,37 @@ def test_workspaces_plans_and_outputs_of_one_call(dev, call):
         del kept
         assert torch.equal(got, want)
     assert rlt.rlt_get_device_error() == 0
+
+
+@pytest.mark.parametrize("call", ["decode", "kv8", "append"])
+def test_a_captured_stream_that_is_not_the_current_one(dev, call):
+    """An output made by the call while another stream than torch's current one is being captured."""
+    import torch
+    import paged_kv_looped_gb300 as rlt
+    import workloads as W
+    from helpers import bf16_dev, i32_dev
+    case = W.custom(B=2, Hq=4, Hkv=2, D=128, ps=16, seq_lens=[100, 37], seed=5)
+    h = W.host_tensors(case)
+    pool = rlt.KVPool(bf16_dev(h.k_pool, dev)[None].contiguous(), bf16_dev(h.v_pool, dev)[None].contiguous())
+    q, pt, sl = bf16_dev(h.q, dev), i32_dev(case.page_table, dev), i32_dev(case.seq_lens, dev)
+    shape = (1, *h.k_pool.shape)
+    pool8 = rlt.KV8Pool(*(torch.zeros(shape, dtype=torch.uint8, device=dev).random_(0, 120).view(torch.float8_e4m3fn)
+                          for _ in range(2)), *(torch.full(shape[:4], 120, dtype=torch.uint8, device=dev) for _ in range(2)))
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    k, pos = torch.randn(2, 2, 128, device=dev).bfloat16(), torch.tensor([100, 37], device=dev)
+    run = {"decode": lambda **kw: rlt.rlt_paged_decode_attn(pool, 0, q, pt, sl, 100, workspace=ws, **kw),
+           "kv8": lambda **kw: rlt.rlt_paged_decode_attn_kv8(pool8, 0, q, pt, sl, 100, workspace=ws, **kw),
+           "append": lambda **kw: rlt.rlt_kv8_append_rope(pool8, 0, k, k, pos, pos, 128, 1e4, q=q, **kw)}[call]
+    want = run()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        torch.empty_like(want)                                  # (its memory is there to be used again)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="relaxed"):
+        with torch.cuda.stream(other):
+            got = run(stream=side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert rlt.rlt_get_device_error() == 0
